@@ -596,6 +596,182 @@ bool same_shape(const fvattn_shape& a, const fvattn_shape& b) {
 
 bool tensor_ok(const void* p) { return p && aligned(p, 16); }
 
+// ---------------------------------------------------------------------------
+// Layer norm.
+// ---------------------------------------------------------------------------
+int norm_args(const fvattn_norm* n, NormArgs* a) {
+  if (!n) return FVATTN_ERR_INVALID_ARG;
+  if (n->dtype != FVATTN_F32 && n->dtype != FVATTN_BF16) return FVATTN_ERR_DTYPE;
+  if (n->rows < 0 || n->rows >= (1ll << 31) || n->channels < 1 || n->channels > 65536 || n->groups < 1 ||
+      n->rows % n->groups)
+    return FVATTN_ERR_SHAPE;
+  if (!(n->eps >= 0.f) || std::isinf(n->eps)) return FVATTN_ERR_INVALID_ARG;
+  if ((n->x_stride != 0 && n->x_stride < n->channels) || (n->y_stride != 0 && n->y_stride < n->channels))
+    return FVATTN_ERR_INVALID_ARG;
+  a->rows = n->rows;
+  a->C = n->channels;
+  a->groups = n->groups;
+  a->rows_per_group = n->rows / n->groups;
+  a->x_stride = n->x_stride ? n->x_stride : n->channels;
+  a->y_stride = n->y_stride ? n->y_stride : n->channels;
+  a->eps = n->eps;
+  a->gain_one = n->gain_one ? 1.f : 0.f;
+  const long long blocks = norm_bwd_blocks(n->rows, n->channels);
+  a->rows_per_block = blocks ? (n->rows + blocks - 1) / blocks : 1;
+  return FVATTN_OK;
+}
+
+// Status word, then the backward's partial column sums.
+size_t norm_ws_bytes(const NormArgs& a) {
+  const long long blocks = a.rows ? (a.rows + a.rows_per_block - 1) / a.rows_per_block : 0;
+  return kAlign + (blocks ? align_up(sizeof(float) * 2 * (size_t)a.C * (size_t)(blocks + a.groups - 1)) : 0);
+}
+
+// ---------------------------------------------------------------------------
+// Sliding-window attention.
+// ---------------------------------------------------------------------------
+int win_geom(const fvattn_window* w, WinGeom* g) {
+  if (!w) return FVATTN_ERR_INVALID_ARG;
+  if (w->dtype != FVATTN_BF16) return FVATTN_ERR_DTYPE;
+  if (w->batch < 1 || w->heads < 1 || w->kv_heads < 1 || w->heads % w->kv_heads || w->q_len < 0 || w->kv_len < 0)
+    return FVATTN_ERR_SHAPE;
+  if (w->q_len > (1 << 28) || w->kv_len > (1 << 28) || (int64_t)w->batch * w->heads > (1 << 20)) return FVATTN_ERR_SHAPE;
+  if (w->head_dim != 64 && w->head_dim != 128) return FVATTN_ERR_SHAPE;
+  if (w->unit < 1 || w->window < 0 || w->sinks < 0) return FVATTN_ERR_INVALID_ARG;
+  if (std::isnan(w->scale) || w->scale < 0.f || std::isinf(w->scale)) return FVATTN_ERR_INVALID_ARG;
+  *g = WinGeom{};
+  g->B = w->batch;
+  g->H = w->heads;
+  g->Hk = w->kv_heads;
+  g->G = w->heads / w->kv_heads;
+  g->D = w->head_dim;
+  g->Nq = w->q_len;
+  g->Nk = w->kv_len;
+  g->unit = w->unit;
+  g->window = w->window;
+  g->sinks = w->sinks;
+  g->scale = w->scale > 0.f ? w->scale : (float)(1.0 / std::sqrt((double)w->head_dim));
+  return FVATTN_OK;
+}
+
+// A view of [B, heads, tokens, D]: pointer, alignment, strides; for an output
+// also that its elements are distinct.
+int check_view(const fvattn_view* t, const WinGeom& g, int heads, int tokens, bool output) {
+  if (!t) return FVATTN_ERR_INVALID_ARG;
+  if (tokens == 0) return FVATTN_OK;
+  if (!tensor_ok(t->data)) return FVATTN_ERR_INVALID_ARG;
+  const int64_t ext[3] = {tokens, heads, g.B}, str[3] = {t->token, t->head, t->batch};
+  for (int i = 0; i < 3; ++i)
+    if (ext[i] > 1 && (str[i] < 8 || str[i] % 8 || str[i] >= (1ll << 39))) return FVATTN_ERR_INVALID_ARG;
+  if (!output) return FVATTN_OK;
+  int64_t reach = g.D;              // elements spanned by the dimensions of smaller stride
+  bool used[3] = {ext[0] == 1, ext[1] == 1, ext[2] == 1};
+  for (int n = 0; n < 3; ++n) {
+    int k = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && (k < 0 || str[i] < str[k])) k = i;
+    if (k < 0) break;
+    if (str[k] < reach) return FVATTN_ERR_INVALID_ARG;
+    reach = str[k] * (ext[k] - 1) + reach;
+    used[k] = true;
+  }
+  return FVATTN_OK;
+}
+
+uint64_t stride_bytes(int64_t stride, int64_t extent) { return extent > 1 ? (uint64_t)stride * 2 : 16; }
+
+// Box of 64 dims x `rows` tokens of one head of a [B, heads, N, D] view,
+// 128-byte swizzle; tokens past N read as zero.  An empty tensor gets a map
+// over `any` that no load uses.
+int make_head_map(CUtensorMap* map, const fvattn_view& t, const WinGeom& g, int heads, int N, int rows,
+                  const void* any) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return FVATTN_ERR_CUDA;
+  const cuuint64_t dims[4] = {(cuuint64_t)g.D, (cuuint64_t)(N > 0 ? N : 1), (cuuint64_t)heads, (cuuint64_t)g.B};
+  const cuuint64_t strides[3] = {stride_bytes(t.token, N), stride_bytes(t.head, heads), stride_bytes(t.batch, g.B)};
+  const cuuint64_t none[3] = {256, 256, 256};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const cuuint64_t dims0[4] = {(cuuint64_t)g.D, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(N > 0 ? t.data : any),
+                         N > 0 ? dims : dims0, N > 0 ? strides : none, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FVATTN_OK : FVATTN_ERR_CUDA;
+}
+
+// The queries: (D, heads of a KV head, tokens, KV heads, B), box 64 dims x
+// `pack` heads x `tokens` tokens, so a tile's rows are (token, head) pairs.
+int make_query_map(CUtensorMap* map, const fvattn_view& t, const WinGeom& g, int pack, int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return FVATTN_ERR_CUDA;
+  const cuuint64_t dims[5] = {(cuuint64_t)g.D, (cuuint64_t)g.G, (cuuint64_t)g.Nq, (cuuint64_t)g.Hk, (cuuint64_t)g.B};
+  const cuuint64_t strides[4] = {stride_bytes(t.head, g.G), stride_bytes(t.token, g.Nq),
+                                 stride_bytes(t.head * g.G, g.Hk), stride_bytes(t.batch, g.B)};
+  const cuuint32_t box[5] = {64, (cuuint32_t)pack, (cuuint32_t)tokens, 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t.data, dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FVATTN_OK : FVATTN_ERR_CUDA;
+}
+
+// SMs the split of few items is made for (a B200's; the workspace's size must
+// not depend on the device that asks for it).
+constexpr int kWinSms = 148;
+
+// Tiling of the forward: heads packed into a tile when a tile of one head's
+// queries would stay partly empty, items of two query tiles unless one holds
+// all queries, and the key tiles split when there are fewer items than SMs
+// (each split at least four key tiles).
+int win_plan(const WinGeom& g, WinFwdArgs* a) {
+  a->g = g;
+  a->pack = g.Nq < 128 && g.G <= 128 ? g.G : 1;
+  a->tokens = 128 / a->pack < g.Nq ? 128 / a->pack : g.Nq;
+  const int tiles = a->tokens ? (g.Nq + a->tokens - 1) / a->tokens : 0;
+  a->dual = tiles > 1;
+  a->item_tiles = a->dual ? (tiles + 1) / 2 : tiles;
+  const int64_t items = (int64_t)g.B * g.Hk * (g.G / a->pack) * a->item_tiles;
+  if (items > (1 << 28)) return FVATTN_ERR_SHAPE;
+  a->splits = 1;
+  if (items > 0 && items < kWinSms) {
+    int64_t keys = g.Nk;
+    if (g.window > 0) {
+      const int64_t w = ((int64_t)g.window + 1) * g.unit + (int64_t)a->tokens * (a->dual ? 2 : 1) +
+                        (int64_t)g.sinks * g.unit;
+      keys = w < keys ? w : keys;
+    }
+    const int64_t most = ((keys + 127) / 128) / 4;
+    const int64_t want = kWinSms / items;
+    a->splits = (int)(most < 1 ? 1 : want < most ? want : most);
+  }
+  a->parts = a->dual ? a->splits : 2 * a->splits;
+  a->n_items = (int)(items * a->splits);
+  return FVATTN_OK;
+}
+
+struct WinWs {
+  size_t counters, part_lse, part_o, total, zeroed;
+};
+WinWs win_ws(const WinFwdArgs& a) {
+  WinWs L{};
+  size_t off = kAlign;               // status word
+  L.zeroed = sizeof(int);
+  if (a.parts > 1) {
+    const size_t rows = (size_t)a.n_items * 2 * a.tokens * a.pack;
+    L.counters = off;
+    const size_t n = sizeof(int) * (size_t)(a.n_items / a.splits) * 2;
+    off = align_up(off + n);
+    L.zeroed = L.counters + n;
+    L.part_lse = off;
+    off = align_up(off + sizeof(float) * rows);
+    L.part_o = off;
+    off = align_up(off + sizeof(float) * rows * a.g.D);
+  }
+  L.total = off;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -981,6 +1157,121 @@ int fvattn_qkv_rope(const fvattn_shape* shape, const void* x, int32_t channels, 
   a.wait_cap = kDefaultWaitCap;
   StageTimer t(FVATTN_STAGE_PROLOGUE, c.s);
   FV_CUDA(launch_qkv(mx, mw, a, variant, c.dev.sms, c.s));
+  t.kernels = 1;
+  return FVATTN_OK;
+}
+
+int fvattn_layer_norm_fwd(const fvattn_norm* norm, const void* x, const float* weight, const float* bias, void* y,
+                          float* mean, float* rstd, fvattn_stream_t stream) {
+  NormArgs a{};
+  FV_TRY(norm_args(norm, &a));
+  if (a.rows > 0 && (!tensor_ok(x) || !tensor_ok(y))) return FVATTN_ERR_INVALID_ARG;
+  if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4)) return FVATTN_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  FV_TRY(device_info(&dev));
+  if (a.rows == 0) return FVATTN_OK;
+  a.w = weight;
+  a.b = bias;
+  a.mean_out = mean;
+  a.rstd_out = rstd;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  StageTimer t(FVATTN_STAGE_NORM, s);
+  FV_CUDA(launch_norm_fwd(a, norm->dtype, x, y, dev.sms, s));
+  t.kernels = 1;
+  return FVATTN_OK;
+}
+
+int fvattn_workspace_size_norm(const fvattn_norm* norm, size_t* bytes) {
+  if (!bytes) return FVATTN_ERR_INVALID_ARG;
+  NormArgs a{};
+  FV_TRY(norm_args(norm, &a));
+  *bytes = norm_ws_bytes(a);
+  return FVATTN_OK;
+}
+
+int fvattn_layer_norm_bwd(const fvattn_norm* norm, const void* x, const void* dy, const float* weight,
+                          const float* mean, const float* rstd, void* dx, float* dweight, float* dbias, void* ws,
+                          size_t ws_bytes, fvattn_stream_t stream) {
+  NormArgs a{};
+  FV_TRY(norm_args(norm, &a));
+  if (!dx && !dweight && !dbias) return FVATTN_ERR_INVALID_ARG;
+  if (a.rows > 0 && (!tensor_ok(x) || !tensor_ok(dy) || !mean || !rstd)) return FVATTN_ERR_INVALID_ARG;
+  if (!aligned(dx, 16) || !aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
+      !aligned(dbias, 4))
+    return FVATTN_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign)) return FVATTN_ERR_INVALID_ARG;
+  if (ws_bytes < norm_ws_bytes(a)) return FVATTN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  FV_TRY(device_info(&dev));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.rows == 0) {                 // sums over no rows
+    const size_t n = sizeof(float) * (size_t)a.groups * a.C;
+    if (dweight) FV_CUDA(cudaMemsetAsync(dweight, 0, n, s));
+    if (dbias) FV_CUDA(cudaMemsetAsync(dbias, 0, n, s));
+    return FVATTN_OK;
+  }
+  a.w = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.partial = dweight || dbias ? reinterpret_cast<float*>(static_cast<char*>(ws) + kAlign) : nullptr;
+  StageTimer t(FVATTN_STAGE_NORM_BWD, s);
+  FV_CUDA(launch_norm_bwd(a, norm->dtype, x, dy, dx, dweight, dbias, dev.sms, s));
+  t.kernels = a.partial ? 2 : 1;
+  return FVATTN_OK;
+}
+
+int fvattn_workspace_size_window(const fvattn_window* win, size_t* bytes) {
+  if (!bytes) return FVATTN_ERR_INVALID_ARG;
+  WinGeom g;
+  WinFwdArgs a{};
+  FV_TRY(win_geom(win, &g));
+  FV_TRY(win_plan(g, &a));
+  *bytes = win_ws(a).total;
+  return FVATTN_OK;
+}
+
+int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvattn_view* k, const fvattn_view* v,
+                      const int32_t* q_lens, const int32_t* kv_lens, const fvattn_view* out, float* lse, void* ws,
+                      size_t ws_bytes, fvattn_stream_t stream) {
+  WinGeom g;
+  WinFwdArgs a{};
+  FV_TRY(win_geom(win, &g));
+  FV_TRY(check_view(q, g, g.H, g.Nq, false));
+  FV_TRY(check_view(k, g, g.Hk, g.Nk, false));
+  FV_TRY(check_view(v, g, g.Hk, g.Nk, false));
+  FV_TRY(check_view(out, g, g.H, g.Nq, true));
+  if ((g.Nq > 0 && !lse) || !aligned(lse, 4) || !aligned(q_lens, 4) || !aligned(kv_lens, 4))
+    return FVATTN_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign)) return FVATTN_ERR_INVALID_ARG;
+  g.q_lens = q_lens;
+  g.kv_lens = kv_lens;
+  FV_TRY(win_plan(g, &a));
+  const WinWs L = win_ws(a);
+  if (ws_bytes < L.total) return FVATTN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  FV_TRY(device_info(&dev));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  FV_CUDA(cudaMemsetAsync(base, 0, L.zeroed, s));
+  if (a.n_items == 0) return FVATTN_OK;
+  CUtensorMap mq, mk, mv;
+  FV_TRY(make_query_map(&mq, *q, g, a.pack, a.tokens));
+  FV_TRY(make_head_map(&mk, *k, g, g.Hk, g.Nk, 128, q->data));
+  FV_TRY(make_head_map(&mv, *v, g, g.Hk, g.Nk, 128, q->data));
+  a.out = out->data;
+  a.o_batch = out->batch;
+  a.o_head = out->head;
+  a.o_token = out->token;
+  a.lse = lse;
+  if (a.parts > 1) {
+    a.part_lse = reinterpret_cast<float*>(base + L.part_lse);
+    a.part_o = reinterpret_cast<float*>(base + L.part_o);
+    a.counters = reinterpret_cast<int*>(base + L.counters);
+  }
+  a.status = reinterpret_cast<int*>(base);
+  a.wait_cap = kDefaultWaitCap;
+  StageTimer t(FVATTN_STAGE_WINDOW, s);
+  FV_CUDA(launch_window_fwd(mq, mk, mv, a, dev.sms, s));
   t.kernels = 1;
   return FVATTN_OK;
 }

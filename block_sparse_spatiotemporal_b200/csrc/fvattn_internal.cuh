@@ -170,6 +170,51 @@ struct BwdArgs {
   long long wait_cap;
 };
 
+// Layer norm (both directions).
+constexpr int kNormBlocks = 296;   // persistent blocks of the backward (two per SM): bounds its partial sums
+struct NormArgs {
+  long long rows, rows_per_group;
+  long long rows_per_block;        // contiguous rows of a block
+  long long x_stride, y_stride;    // elements
+  int C, groups;
+  int warps;                       // of the team that holds a row
+  float eps, gain_one;             // gain = w + gain_one
+  const float* w;                  // [groups, C] or null
+  const float* b;
+  float* mean_out;                 // forward: [rows] or null
+  float* rstd_out;
+  const float* mean;               // backward: [rows]
+  const float* rstd;
+  float* partial;                  // backward: [blocks + groups - 1][2][C] column sums, or null
+};
+
+// Sliding-window attention.
+struct WinGeom {
+  int B, H, Hk, G, D;              // G = H / Hk query heads per KV head
+  int Nq, Nk;
+  int unit, window, sinks;
+  float scale;
+  const int* q_lens;               // [B] or null
+  const int* kv_lens;
+};
+struct WinFwdArgs {
+  WinGeom g;
+  int dual;                        // 1: items of two query tiles; 0: one, both groups on it
+  int pack;                        // query heads of a KV head in one tile: 1 or G
+  int tokens;                      // queries of a tile
+  int item_tiles;                  // items per (batch, KV head, head slot)
+  int splits, parts;               // of an item's key tiles; parts written and joined (1: none)
+  int n_items;
+  void* out;
+  long long o_batch, o_head, o_token;
+  float* lse;                      // [B, H, Nq]
+  float* part_o;                   // [n_items][2][tokens * pack][D]
+  float* part_lse;                 // [n_items][2][tokens * pack], base 2
+  int* counters;
+  int* status;
+  long long wait_cap;
+};
+
 struct FineF32Args {
   Geom g;
   const float* q;
@@ -556,6 +601,12 @@ cudaError_t launch_bwd(const CUtensorMap& s0, const CUtensorMap& s1, const CUten
 cudaError_t launch_augment(const Geom& g, const float* S, const int* counts, const int* idx, int cap,
                            const int* ucount, const int* worklist, int G, const long long* busy, int fill_percent,
                            int* extra, int* out_counts, int* out_idx, int out_cap, int* status, cudaStream_t s);
+long long norm_bwd_blocks(long long rows, int C);
+cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const void* x, void* y, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const void* x, const void* dy, void* dx, float* dw, float* db,
+                            int num_sms, cudaStream_t s);
+cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
+                              int num_sms, cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, long long cap, cudaStream_t s);
 
 }  // namespace fvattn

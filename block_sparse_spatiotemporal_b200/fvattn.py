@@ -9,6 +9,7 @@ Names follow the C ABI in include/fvattn.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -24,6 +25,8 @@ __all__ = [
     "device_status", "selftest_wait_timeout", "new_blocks", "new_cache", "profile_enable", "profile_read",
     "STAGES", "pool_select_noalloc", "noalloc_status", "profile_cta_times", "workspace_size_qkv", "qkv_rope", "workspace_size_bwd", "block_sparse_bwd",
     "augment_lists", "block_sparse_fwd_worklist", "timestep_params",
+    "Norm", "Window", "View", "make_norm", "norm_workspace", "layer_norm_fwd", "layer_norm_bwd",
+    "make_window", "window_workspace", "window_fwd",
 ]
 
 F32, BF16 = 0, 1
@@ -70,6 +73,24 @@ class Blocks(ctypes.Structure):
 class MaskCache(ctypes.Structure):
     _fields_ = [("blocks", Blocks), ("shape", Shape), ("top_p", ctypes.c_float),
                 ("k_min", ctypes.c_int32), ("valid", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("gain_one", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class Window(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("q_len", ctypes.c_int32), ("kv_len", ctypes.c_int32),
+                ("unit", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("token", ctypes.c_int64)]
 
 
 _LIB = None
@@ -120,6 +141,14 @@ _SIGS = {
     "fvattn_qkv_rope": [ctypes.POINTER(Shape), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                         ctypes.POINTER(Rope), ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
+    "fvattn_layer_norm_fwd": [ctypes.POINTER(Norm), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+    "fvattn_workspace_size_norm": [ctypes.POINTER(Norm), ctypes.POINTER(ctypes.c_size_t)],
+    "fvattn_layer_norm_bwd": [ctypes.POINTER(Norm)] + [ctypes.c_void_p] * 9 + [ctypes.c_size_t, ctypes.c_void_p],
+    "fvattn_workspace_size_window": [ctypes.POINTER(Window), ctypes.POINTER(ctypes.c_size_t)],
+    "fvattn_window_fwd": [ctypes.POINTER(Window), ctypes.POINTER(View), ctypes.POINTER(View), ctypes.POINTER(View),
+                          ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(View), ctypes.c_void_p, ctypes.c_void_p,
+                          ctypes.c_size_t, ctypes.c_void_p],
     "fvattn_get_device_status": [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)],
     "fvattn_selftest_wait_timeout": [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_void_p],
     "fvattn_profile_enable": [ctypes.c_int],
@@ -127,7 +156,8 @@ _SIGS = {
     "fvattn_status_string": [ctypes.c_int],
 }
 
-STAGES = ("tables", "reorder", "pool", "select", "schedule", "fine", "prologue", "bwd_prep", "bwd_kv", "bwd_q")
+STAGES = ("tables", "reorder", "pool", "select", "schedule", "fine", "prologue", "bwd_prep", "bwd_kv", "bwd_q",
+          "norm", "norm_bwd", "window")
 
 
 def lib():
@@ -412,6 +442,179 @@ def qkv_rope(shape: Shape, x, w, ws, bias=None, rope: Optional[Rope] = None, t_o
            lib().fvattn_qkv_rope(ctypes.byref(shape), _ptr(x), int(C), _ptr(w), _ptr(bias), _rope_ptr(rope),
                                  int(t_offset), _ptr(q), _ptr(k), _ptr(v), _ptr(ws), ws.numel(), _stream(stream)))
     return q, k, v
+
+
+@contextlib.contextmanager
+def _launch(tensors, stream: Optional[torch.cuda.Stream]):
+    """The tensors' device made current, with the stream to launch on (the
+    given one, or the device's current one; new outputs belong to it)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("expected every tensor on one device")
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        with torch.cuda.stream(s):
+            yield ctypes.c_void_p(s.cuda_stream)
+
+
+def _typed(t: Optional[torch.Tensor], dtype, shape, what: str):
+    """Pointer of a contiguous tensor of this dtype and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _torch_dtype(dtype: int):
+    return torch.bfloat16 if dtype == BF16 else torch.float32
+
+
+def make_norm(rows, channels, groups=1, dtype=BF16, eps=1e-6, gain_one=False, x_stride=0, y_stride=0) -> Norm:
+    """Layer norm of `rows` rows; strides in elements (0: channels)."""
+    return Norm(int(rows), int(channels), int(groups), dtype, 1 if gain_one else 0, float(eps), int(x_stride),
+                int(y_stride))
+
+
+def norm_workspace(norm: Norm, device="cuda") -> torch.Tensor:
+    """A device workspace for layer_norm_bwd (caller-owned)."""
+    n = ctypes.c_size_t()
+    _check("fvattn_workspace_size_norm", lib().fvattn_workspace_size_norm(ctypes.byref(norm), ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _rows(t: Optional[torch.Tensor], norm: Norm, stride: int, what: str):
+    """Pointer of the rows of t: contiguous [..., channels], or [rows, channels] with norm's row stride."""
+    if t is None:
+        return None
+    stride = stride or norm.channels
+    ok = t.dtype == _torch_dtype(norm.dtype) and t.dim() >= 1 and t.shape[-1] == norm.channels and \
+        t.numel() == norm.rows * norm.channels
+    if ok and t.numel() > 0:
+        if t.is_contiguous():
+            ok = stride == norm.channels or norm.rows == 1
+        else:
+            ok = t.dim() == 2 and (t.stride(1) == 1 or norm.channels == 1) and (norm.rows == 1 or t.stride(0) == stride)
+    if not ok:
+        raise ValueError(f"{what}: expected {norm.rows} {_torch_dtype(norm.dtype)} rows of {norm.channels} "
+                         f"with row stride {stride}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
+    """An output like `like` with norm's row stride."""
+    if stride in (0, norm.channels) or norm.rows <= 1:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    buf = torch.empty(norm.rows * stride, dtype=like.dtype, device=like.device)
+    return buf.as_strided((norm.rows, norm.channels), (stride, 1))
+
+
+def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x ([..., channels]) with weight and bias
+    [groups, channels] float32 (or None): returns (y, mean, rstd)."""
+    affine = (norm.groups, norm.channels)
+    with _launch((x, weight, bias, y, mean, rstd), stream) as s:
+        px = _rows(x, norm, norm.x_stride, "x")
+        if y is None:
+            y = _new_rows(x, norm, norm.y_stride)
+        if mean is None:
+            mean = torch.empty(norm.rows, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(norm.rows, dtype=torch.float32, device=x.device)
+        _check("fvattn_layer_norm_fwd",
+               lib().fvattn_layer_norm_fwd(ctypes.byref(norm), px, _typed(weight, torch.float32, affine, "weight"),
+                                           _typed(bias, torch.float32, affine, "bias"),
+                                           _rows(y, norm, norm.y_stride, "y"),
+                                           _typed(mean, torch.float32, (norm.rows,), "mean"),
+                                           _typed(rstd, torch.float32, (norm.rows,), "rstd"), s))
+    return y, mean, rstd
+
+
+def layer_norm_bwd(norm: Norm, x, dy, mean, rstd, ws, weight=None, grads=None, stream=None):
+    """Backward of layer_norm_fwd: returns (dx, dweight, dbias).  grads: the
+    three output tensors, None for a gradient that is not wanted."""
+    affine = (norm.groups, norm.channels)
+    with _launch((x, dy, mean, rstd, ws, weight, *(grads or ())), stream) as s:
+        if grads is None:
+            grads = (_new_rows(x, norm, norm.x_stride),
+                     torch.empty(affine, dtype=torch.float32, device=x.device),
+                     torch.empty(affine, dtype=torch.float32, device=x.device))
+        dx, dw, db = grads
+        _check("fvattn_layer_norm_bwd",
+               lib().fvattn_layer_norm_bwd(ctypes.byref(norm), _rows(x, norm, norm.x_stride, "x"),
+                                           _rows(dy, norm, norm.y_stride, "dy"),
+                                           _typed(weight, torch.float32, affine, "weight"),
+                                           _typed(mean, torch.float32, (norm.rows,), "mean"),
+                                           _typed(rstd, torch.float32, (norm.rows,), "rstd"),
+                                           _rows(dx, norm, norm.x_stride, "dx"),
+                                           _typed(dw, torch.float32, affine, "dweight"),
+                                           _typed(db, torch.float32, affine, "dbias"), _ptr(ws), ws.numel(), s))
+    return dx, dw, db
+
+
+def make_window(batch, heads, head_dim, q_len, kv_len, window, sinks=0, unit=1, kv_heads=None, dtype=BF16,
+                scale=0.0) -> Window:
+    """Sliding-window attention: `window` units of `unit` tokens (0: every
+    earlier one) and the first `sinks` units."""
+    return Window(int(batch), int(heads), int(heads if kv_heads is None else kv_heads), int(head_dim), int(q_len),
+                  int(kv_len), int(unit), int(window), int(sinks), dtype, float(scale))
+
+
+def window_workspace(win: Window, device="cuda") -> torch.Tensor:
+    """A device workspace for window_fwd (caller-owned)."""
+    n = ctypes.c_size_t()
+    _check("fvattn_workspace_size_window", lib().fvattn_workspace_size_window(ctypes.byref(win), ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _view(t: torch.Tensor, batch: int, heads: int, tokens: int, d: int, what: str):
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (batch, heads, tokens, d) or (t.numel() and t.stride(3) != 1):
+        raise ValueError(f"{what}: expected a bfloat16 tensor [{batch}, {heads}, {tokens}, {d}] with contiguous rows")
+    return ctypes.byref(View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _new_heads(like: torch.Tensor, lens):
+    """An output shaped and laid out like `like`; rows behind a sequence's
+    length are not written by the library, so with lengths they start as 0."""
+    new = torch.empty_strided if lens is None else _zeros_strided
+    dense = like.is_contiguous() or like.transpose(1, 2).is_contiguous()
+    strides = like.stride() if dense else torch.empty(like.shape, device="meta").stride()
+    return new(like.shape, strides, dtype=like.dtype, device=like.device)
+
+
+def _zeros_strided(shape, strides, dtype, device):
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device).zero_()
+
+
+def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, lse=None, stream=None):
+    """Sliding-window attention of q [B, heads, q_len, d] over k, v
+    [B, kv_heads, kv_len, d] (any strides with contiguous rows): returns
+    (out, lse).  q_lens, kv_lens: int32 device tensors [B] or None."""
+    B, H, Hk, D = win.batch, win.heads, win.kv_heads, win.head_dim
+    with _launch((q, k, v, ws, q_lens, kv_lens, out, lse), stream) as s:
+        vq = _view(q, B, H, win.q_len, D, "q")
+        if out is None:
+            out = _new_heads(q, q_lens)
+        if lse is None:
+            lse = (torch.empty if q_lens is None else torch.zeros)((B, H, win.q_len), dtype=torch.float32,
+                                                                   device=q.device)
+        _check("fvattn_window_fwd",
+               lib().fvattn_window_fwd(ctypes.byref(win), vq, _view(k, B, Hk, win.kv_len, D, "k"),
+                                       _view(v, B, Hk, win.kv_len, D, "v"),
+                                       _typed(q_lens, torch.int32, (B,), "q_lens"),
+                                       _typed(kv_lens, torch.int32, (B,), "kv_lens"),
+                                       _view(out, B, H, win.q_len, D, "out"),
+                                       _typed(lse, torch.float32, (B, H, win.q_len), "lse"), _ptr(ws), ws.numel(), s))
+    return out, lse
 
 
 def device_status(ws, stream=None) -> int:

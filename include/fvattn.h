@@ -330,6 +330,91 @@ int fvattn_qkv_rope(const fvattn_shape* shape, const void* x, int32_t channels, 
                     const float* bias, const fvattn_rope* rope, int32_t t_offset, void* q, void* k,
                     void* v, void* ws, size_t ws_bytes, fvattn_stream_t stream);
 
+/* Layer norm of the rows in front of the QKV projection (x of
+ * fvattn_qkv_rope), forward and backward, with an affine per group of
+ * consecutive rows: groups = 1 is the plain layer norm, groups = batch or
+ * batch * frames the timestep modulation of a DiT block (one scale and shift
+ * per sample or per latent frame).
+ *   x, y, dy, dx: `rows` rows of `channels` values, float32 or bf16 (dtype);
+ *     row r of x and dx starts x_stride elements after row r - 1, of y and dy
+ *     y_stride (0 = channels; at least channels).  Any element alignment of
+ *     the rows is taken; strides and channels that are multiples of 16 bytes
+ *     are the fast ones.
+ *   weight, bias: [groups, channels] float32, either may be NULL (1 and 0).
+ *     Row r belongs to group r / (rows / groups); its gain is weight, or
+ *     1 + weight with gain_one != 0.
+ *   mean, rstd: [rows] float32.  mean = sum x / C, rstd = 1 / sqrt(var + eps),
+ *     var = sum (x - mean)^2 / C; either may be NULL in the forward.
+ * Forward:  y = (x - mean) rstd gain + bias, rounded once to dtype.
+ * Backward: with xhat = (x - mean) rstd and gy = dy gain,
+ *   dx = rstd (gy - sum gy / C - xhat sum(gy xhat) / C),
+ *   dweight = sum dy xhat and dbias = sum dy over each group's rows
+ *   ([groups, channels] float32, overwritten).  Each of dx, dweight, dbias
+ *   may be NULL when it is not wanted.  Deterministic (no atomics).
+ * y may be x and dx may be dy or x where their strides are equal; otherwise
+ * outputs must not overlap inputs.  rows may be 0 (the sums are then 0).
+ * Limits: rows < 2^31 and a multiple of groups, channels in [1, 65536],
+ * groups >= 1, eps >= 0 and finite.  The forward needs no workspace; the
+ * backward takes fvattn_workspace_size_norm bytes. */
+typedef struct {
+  int64_t rows;
+  int32_t channels, groups;
+  fvattn_dtype dtype;
+  int32_t gain_one;
+  float eps;
+  int64_t x_stride, y_stride;
+} fvattn_norm;
+int fvattn_layer_norm_fwd(const fvattn_norm* norm, const void* x, const float* weight, const float* bias, void* y,
+                          float* mean, float* rstd, fvattn_stream_t stream);
+int fvattn_workspace_size_norm(const fvattn_norm* norm, size_t* bytes);
+int fvattn_layer_norm_bwd(const fvattn_norm* norm, const void* x, const void* dy, const float* weight,
+                          const float* mean, const float* rstd, void* dx, float* dweight, float* dbias, void* ws,
+                          size_t ws_bytes, fvattn_stream_t stream);
+
+/* Causal attention with a sliding window and sinks, beside the block-sparse
+ * attention: streaming video, where a latent frame attends to itself, the
+ * frames of a window before it and a few first frames that stay visible
+ * (unit = tokens of a frame), and token sequences (unit = 1).  Query i of a
+ * sequence stands at position p = i + kv_len - q_len (the last query is at
+ * the last key) and sees key j when, with u(x) = floor(x / unit),
+ *   u(j) <= u(p)  and  (window == 0  or  u(p) - u(j) < window  or  u(j) < sinks).
+ * out = softmax(scale q k^T over the visible keys) v and lse the natural log
+ * of the softmax's normaliser; a query that sees no key (none in the cache,
+ * or a position before the first key) gets out = 0 and lse = -inf.
+ *   q, out [B, heads, q_len, head_dim]; k, v [B, kv_heads, kv_len, head_dim];
+ *   query head h reads KV head h / (heads / kv_heads); lse [B, heads, q_len]
+ *   float32, contiguous.  bf16, head_dim 64 or 128, fp32 sums and softmax;
+ *   the probabilities are rounded to bf16 for the tensor cores.
+ * q_lens, kv_lens: NULL, or DEVICE arrays [B] int32 of each sequence's own
+ *   lengths in [0, q_len] and [0, kv_len] (a length outside is cut to that
+ *   range).  Rows of out and lse behind a sequence's q_lens are not written;
+ *   k and v that no query of the sequence sees (behind its kv_lens, or
+ *   between sinks and the first query's window) may hold anything, NaN
+ *   included.  Visible k and v must be finite for the others to stay so: a
+ *   NaN that only some queries of a sequence see can reach its other queries.
+ * Few queries (single tokens against a cache) split the keys over the GPU
+ * and join the parts in a fixed order: every result is deterministic. */
+typedef struct {
+  int32_t batch, heads, kv_heads, head_dim;
+  int32_t q_len, kv_len;
+  int32_t unit;           /* tokens per unit of the window, >= 1 */
+  int32_t window;         /* units a query sees, its own included; 0 = all before it */
+  int32_t sinks;          /* first units that stay visible */
+  fvattn_dtype dtype;     /* FVATTN_BF16 */
+  float scale;            /* 0 => 1/sqrt(head_dim) */
+} fvattn_window;
+/* A [B, heads, tokens, head_dim] tensor: strides in elements, positive
+ * multiples of 8 (ignored for extents of 1), head_dim contiguous, data
+ * 16-byte aligned.  Outputs must not overlap themselves or any input. */
+typedef struct {
+  void* data;
+  int64_t batch, head, token;
+} fvattn_view;
+int fvattn_workspace_size_window(const fvattn_window* win, size_t* bytes);
+int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvattn_view* k, const fvattn_view* v,
+                      const int32_t* q_lens, const int32_t* kv_lens, const fvattn_view* out, float* lse, void* ws,
+                      size_t ws_bytes, fvattn_stream_t stream);
+
 /* Synchronises the stream, reads and clears the workspace status word.
  * *status is 0 or a positive code: 1 bad block id, 2 wait cap reached. */
 int fvattn_get_device_status(void* ws, fvattn_stream_t stream, int32_t* status);
@@ -359,7 +444,10 @@ typedef enum {
   FVATTN_STAGE_BWD_PREP = 7,  /* backward: D = rowsum(dout * out), lse * log2(e) */
   FVATTN_STAGE_BWD_KV = 8,    /* backward: key-stationary dK, dV kernel */
   FVATTN_STAGE_BWD_Q = 9,     /* backward: query-stationary dQ kernel */
-  FVATTN_STAGE_COUNT = 10
+  FVATTN_STAGE_NORM = 10,     /* layer norm, forward */
+  FVATTN_STAGE_NORM_BWD = 11, /* layer norm, backward */
+  FVATTN_STAGE_WINDOW = 12,   /* sliding-window attention, forward */
+  FVATTN_STAGE_COUNT = 13
 } fvattn_stage;
 int fvattn_profile_enable(int enable);
 int fvattn_profile_read(double* ms, int64_t* launches);
