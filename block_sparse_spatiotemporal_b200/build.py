@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cu", "order.cu", "coarse.cu", "scores_tc.cu", "subblock.cu", "schedule.cu", "fine_tc.cu", "fine_q.cu", "fine_f32.cu", "qkv_tc.cu", "bwd_tc.cu", "augment.cu", "selftest.cu", "noalloc.cu",
            "norm.cu", "window_fwd.cu"]
-HEADERS = [os.path.join(CSRC, "fvattn_internal.cuh"), os.path.join(CSRC, "window.cuh"), os.path.join(ROOT, "include", "fvattn.h")]
+HEADERS = [os.path.join(CSRC, "fvattn_internal.cuh"), os.path.join(CSRC, "packed.cuh"),
+           os.path.join(CSRC, "window.cuh"), os.path.join(ROOT, "include", "fvattn.h")]
 LIB = os.path.join(HERE, "libfvattn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -610,13 +610,14 @@ int norm_args(const fvattn_norm* n, NormArgs* a) {
     return FVATTN_ERR_INVALID_ARG;
   a->rows = n->rows;
   a->C = n->channels;
+  a->inv_c = 1.f / (float)n->channels;
   a->groups = n->groups;
   a->rows_per_group = n->rows / n->groups;
   a->x_stride = n->x_stride ? n->x_stride : n->channels;
   a->y_stride = n->y_stride ? n->y_stride : n->channels;
   a->eps = n->eps;
   a->gain_one = n->gain_one ? 1.f : 0.f;
-  const long long blocks = norm_bwd_blocks(n->rows, n->channels);
+  const long long blocks = norm_bwd_blocks(n->rows);
   a->rows_per_block = blocks ? (n->rows + blocks - 1) / blocks : 1;
   return FVATTN_OK;
 }

@@ -171,13 +171,15 @@ struct BwdArgs {
 };
 
 // Layer norm (both directions).
-constexpr int kNormBlocks = 296;   // persistent blocks of the backward (two per SM): bounds its partial sums
+constexpr int kNormBlocks = 148;   // persistent blocks of the backward (one per SM): bounds its partial sums
 struct NormArgs {
   long long rows, rows_per_group;
   long long rows_per_block;        // contiguous rows of a block
   long long x_stride, y_stride;    // elements
   int C, groups;
   int warps;                       // of the team that holds a row
+  int flat;                        // forward: groups numbered through blockIdx.x
+  float inv_c;                     // 1 / C
   float eps, gain_one;             // gain = w + gain_one
   const float* w;                  // [groups, C] or null
   const float* b;
@@ -601,7 +603,7 @@ cudaError_t launch_bwd(const CUtensorMap& s0, const CUtensorMap& s1, const CUten
 cudaError_t launch_augment(const Geom& g, const float* S, const int* counts, const int* idx, int cap,
                            const int* ucount, const int* worklist, int G, const long long* busy, int fill_percent,
                            int* extra, int* out_counts, int* out_idx, int out_cap, int* status, cudaStream_t s);
-long long norm_bwd_blocks(long long rows, int C);
+long long norm_bwd_blocks(long long rows);
 cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const void* x, void* y, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const void* x, const void* dy, void* dx, float* dw, float* db,
                             int num_sms, cudaStream_t s);

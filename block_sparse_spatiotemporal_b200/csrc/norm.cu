@@ -8,33 +8,53 @@
 // Bound by memory: x is read and y written once (forward), x and dy are read
 // and dx written once (backward).
 //
-// A row is held in the registers of a team of up to 16 warps, 16 elements a
-// thread, so the variance is a second pass over registers and not over
-// memory, and a thread keeps the same columns for all its rows: gain, bias
-// and the backward's column sums stay in registers too.  Blocks walk
-// contiguous row ranges of equal length (persistent grid) and load the next
-// row before they reduce the current one.  The column sums of block c over
-// its rows of group g go to partial slot c + g: the ranges and the groups
-// are both ascending, so every (c, g) pair that meets has a slot of its own,
-// and a second kernel adds a group's slots in ascending order (no atomics,
-// the same bits every run).  Rows wider than 16 warps hold (8192 elements)
-// take the wide kernels, which pass over the row again from L2.
-#include "fvattn_internal.cuh"
+// Forward: a block takes two rows of one group at once and holds them in
+// registers, 32 elements a thread in vectors of 4: gain and bias are then one
+// fully coalesced 16-byte load a vector, shared by both rows.  They come from
+// L1, and there lies the limit next to the memory: at 33,280 x 5,120 bf16
+// (104 us of memory at a copy's rate) one row a block took 135 us, two 119,
+// 103 with gain and bias left out; vectors of 8, which read every other 16
+// bytes of the gain, took 149.  Where so few rows come that the SMs hold them
+// all at once, a row is spread thin (8 a thread) for the latency.
+// The variance never subtracts large sums: a row is shifted by its first
+// element, each thread takes the mean and the squared differences of its own
+// elements, and the parts are joined by
+// M2 = sum M2_i + sum n_i (mean_i - mean)^2, with one barrier a row.
+//
+// Backward: the column sums stay in the registers of a thread, which keeps
+// its columns (and their gain) for all its rows.  Blocks walk contiguous row
+// ranges of equal length (persistent grid), their teams taking the rows in
+// turn; rows arrive through a ring in shared memory that each thread fills
+// with asynchronous copies of its own elements (no barrier: it reads only
+// what it copied), and the second pass over a row reads the ring again.  The
+// sums of block c over its rows of group g are added over its teams in shared
+// memory and go to partial slot c + g: the ranges and the groups are both
+// ascending, so every (c, g) pair that meets has a slot of its own, and a
+// second kernel adds a group's slots in ascending order (no atomics, the same
+// bits every run).
+//
+// Rows wider than 8192 elements take the wide kernels, which pass over the
+// row again from L2.
+#include "packed.cuh"
 
 namespace fvattn {
 namespace ln {
 
-constexpr int EPT = 16;          // elements of a row per thread
-constexpr int MAX_WARPS = 16;    // warps of a team
-constexpr int MAX_C = EPT * 32 * MAX_WARPS;
-constexpr int TEAMS1 = 8;        // one-warp teams per block
+using namespace pk;
+
+constexpr int MAX_C = 8192;      // widest row of the team kernels
+constexpr int MAX_WARPS = 32;    // warps of a team (8 elements a thread; 8 with 32)
+constexpr int MAX_TEAMS = 15;    // teams of a block: one named barrier each
 constexpr int WIDE = 1024;       // threads of a wide row's block
+// rows in the backward's ring, the one at work among them
+template <typename T> constexpr int stages() { return sizeof(T) == 4 ? 2 : 3; }
 
 // VEC consecutive elements as loaded.
 template <typename T, int VEC> struct Raw;
 template <> struct Raw<float, 4> { using type = float4; };
 template <> struct Raw<float, 1> { using type = float; };
 template <> struct Raw<__nv_bfloat16, 8> { using type = uint4; };
+template <> struct Raw<__nv_bfloat16, 4> { using type = uint2; };
 template <> struct Raw<__nv_bfloat16, 2> { using type = uint32_t; };
 template <> struct Raw<__nv_bfloat16, 1> { using type = unsigned short; };
 
@@ -46,6 +66,7 @@ __device__ inline void unpack(const uint4& r, float* v) {
   v[0] = lo16(r.x); v[1] = hi16(r.x); v[2] = lo16(r.y); v[3] = hi16(r.y);
   v[4] = lo16(r.z); v[5] = hi16(r.z); v[6] = lo16(r.w); v[7] = hi16(r.w);
 }
+__device__ inline void unpack(const uint2& r, float* v) { v[0] = lo16(r.x); v[1] = hi16(r.x); v[2] = lo16(r.y); v[3] = hi16(r.y); }
 __device__ inline void unpack(const uint32_t& r, float* v) { v[0] = lo16(r); v[1] = hi16(r); }
 __device__ inline void unpack(const unsigned short& r, float* v) { v[0] = lo16(r); }
 __device__ inline uint32_t pack2(float a, float b) {
@@ -57,8 +78,12 @@ __device__ inline void pack(const float* v, float& r) { r = v[0]; }
 __device__ inline void pack(const float* v, uint4& r) {
   r = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
+__device__ inline void pack(const float* v, uint2& r) { r = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3])); }
 __device__ inline void pack(const float* v, uint32_t& r) { r = pack2(v[0], v[1]); }
 __device__ inline void pack(const float* v, unsigned short& r) { r = (unsigned short)(pack2(v[0], 0.f) & 0xFFFFu); }
+
+__device__ inline float to_f(float v) { return v; }
+__device__ inline float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 __device__ inline float warp_sum(float v) {
 #pragma unroll
@@ -66,22 +91,12 @@ __device__ inline float warp_sum(float v) {
   return v;
 }
 
-// Sums of a and b over the team; red is the team's [2][MAX_WARPS] buffer,
-// free again after the block's next barrier.
-__device__ inline void team_sum2(float& a, float& b, float (*red)[MAX_WARPS], int warps, int warp, int lane) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (warps == 1) return;
-  if (lane == 0) {
-    red[0][warp] = a;
-    red[1][warp] = b;
-  }
-  __syncthreads();
-  a = b = 0.f;
-  for (int i = 0; i < warps; ++i) {
-    a += red[0][i];
-    b += red[1][i];
-  }
+// Meets the warps of one team of the block.
+__device__ inline void team_sync(int warps, int id) {
+  if (warps == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(32 * warps) : "memory");
 }
 
 struct Range {
@@ -94,215 +109,429 @@ __device__ inline Range block_rows(const NormArgs& a) {
   return {r0, r1 < a.rows ? r1 : a.rows};
 }
 
-// A thread's vectors of one row: vector v of thread t is number v * team + t.
-template <typename T, int VEC>
-__device__ inline void load_row(const T* p, int nvec, int t, int team, typename Raw<T, VEC>::type (&x)[EPT / VEC]) {
-  using R = typename Raw<T, VEC>::type;
-#pragma unroll
-  for (int v = 0; v < EPT / VEC; ++v)
-    if (v * team + t < nvec) x[v] = __ldcs(reinterpret_cast<const R*>(p) + v * team + t);
+template <int BYTES>
+__device__ inline void copy_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
+__device__ inline void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ inline void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The thread's columns of gain (or 1 + w) and bias of group g.
-template <int VEC>
-__device__ inline void load_affine(const float* p, float none, float add, long long g, int C, int nvec, int t, int team,
-                                   float (&w)[EPT]) {
-#pragma unroll
-  for (int v = 0; v < EPT / VEC; ++v)
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      w[v * VEC + i] = p && v * team + t < nvec ? p[g * C + (v * team + t) * VEC + i] + add : none;
-}
+// Which vectors of a row a thread holds: warp w of the team the 32 NV vectors
+// from 32 NV w on, its lane l every 32nd of them from l on, so that a thread's
+// addresses differ by constants.  FULL: the row fills every thread.  Otherwise
+// a vector past the row's end stands for the row's last one, so that loads
+// need no branch (one branch a vector kept the loads from being issued
+// together: 33,280 x 5,120 bf16 took 240 us so), and its values are masked.
+template <bool FULL> struct Place {
+  int first, nvec;
+  __device__ bool on(int k) const { return FULL || first + 32 * k < nvec; }
+  __device__ int at(int k) const { return FULL || first + 32 * k < nvec ? first + 32 * k : nvec - 1; }
+};
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(32 * MAX_WARPS)
-    norm_fwd_kernel(const NormArgs a, const T* __restrict__ x, T* __restrict__ y) {
+// The ring of one tensor's rows, a slot of its own for every vector of every
+// thread.  Where a vector is a single bf16 there is no copy that small: the
+// team copies the row's aligned words instead (WORDS), one element further on
+// in shared memory when the row starts inside a word, and meets before it
+// reads them.
+template <typename T, int VEC, int EPT, bool FULL> struct Ring {
   using R = typename Raw<T, VEC>::type;
-  constexpr int NV = EPT / VEC;
-  __shared__ float red[2][2][MAX_WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = a.warps, team = warps * 32, teams = (int)blockDim.x / team;
-  const int t = warps == 1 ? lane : (int)threadIdx.x;
-  const int nvec = a.C / VEC;
-  const float inv_c = 1.f / (float)a.C;
-  const Range rg = block_rows(a);
-  long long r = rg.r0 + (teams > 1 ? warp : 0);
-  long long cur_g = -1;
-  float w[EPT], b[EPT];
-  R nx[NV];
-  if (r < rg.r1) load_row<T, VEC>(x + r * a.x_stride, nvec, t, team, nx);
-  for (; r < rg.r1; r += teams) {
-    float d[EPT];
-    float s = 0.f, s1 = 0.f, s2 = 0.f;
+  static constexpr int NV = EPT / VEC, STAGES = stages<T>();
+  static constexpr bool WORDS = sizeof(T) * VEC < 4;
+  static __host__ __device__ constexpr int bytes(int team) { return EPT * (int)sizeof(T) * team + (WORDS ? 16 : 0); }
+  unsigned char* base;               // the team's ring
+  Place<FULL> pl;
+  int team, t, C;
+  __device__ unsigned char* stage(int s) const { return base + s * bytes(team); }
+  __device__ void fetch(int s, const T* row) const {
+    unsigned char* dst = stage(s);
+    if constexpr (WORDS) {
+      const int odd = (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1);
+      const T* w0 = row - odd;       // aligned word that holds the row's first element
+      const int n = C + odd;         // elements from there to the row's end
+      for (int i = t; i < n / 2; i += team)
+        if (i > 0 || odd == 0) copy_async<4>(dst + 4 * i, w0 + 2 * i);
+      // elements alone in their word: the first after an odd start, the last before an odd end
+      if (odd && t == 0) reinterpret_cast<unsigned short*>(dst)[1] = *reinterpret_cast<const unsigned short*>(row);
+      if ((n & 1) && t == team - 1)
+        reinterpret_cast<unsigned short*>(dst)[n - 1] = *reinterpret_cast<const unsigned short*>(w0 + n - 1);
+    } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (v * team + t < nvec) {
-        unpack(nx[v], d + v * VEC);
-      } else {
+      for (int v = 0; v < NV; ++v)
+        copy_async<(int)sizeof(R)>(dst + (pl.first + 32 * v) * sizeof(R), reinterpret_cast<const R*>(row) + pl.at(v));
+    }
+  }
+  __device__ R get(int s, int v, const T* row) const {
+    if constexpr (WORDS)
+      return *reinterpret_cast<const R*>(stage(s) + 2 * (pl.at(v) + (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1)));
+    else
+      return *reinterpret_cast<const R*>(stage(s) + (pl.first + 32 * v) * sizeof(R));
+  }
+};
+
+// Values a thread keeps: team, place in it.
+struct Lane {
+  int lane, warp, warps, team, teams, id, t;
+  __device__ Lane(int warps_)
+      : lane(threadIdx.x & 31), warp(threadIdx.x >> 5), warps(warps_), team(32 * warps_), teams(1), id(0),
+        t((int)threadIdx.x) {
+    if ((int)blockDim.x != team) {
+      teams = (int)blockDim.x / team;
+      id = (int)threadIdx.x / team;
+      t = (int)threadIdx.x - id * team;
+    }
+  }
+};
+
+// The thread's elements in chunks of packed pairs: a chunk is one vector, or
+// two single elements.
+template <typename T, int VEC, int EPT, bool FULL> struct Chunks {
+  using R = typename Raw<T, VEC>::type;
+  static constexpr int CE = VEC == 1 ? 2 : VEC;      // elements of a chunk
+  static constexpr int NP = CE / 2, N = EPT / CE, VC = VEC == 1 ? 2 : 1;   // vectors of a chunk
+  struct Part {
+    R v[VC];
+  };
+  Place<FULL> pl;
+  // 64-bit mask of pair i's existing elements
+  __device__ uint64_t mask(int k) const {
+    if constexpr (FULL) return ~0ull;
+    if constexpr (VEC == 1)
+      return (pl.on(2 * k) ? 0xFFFFFFFFull : 0ull) | (pl.on(2 * k + 1) ? 0xFFFFFFFF00000000ull : 0ull);
+    else
+      return pl.on(k) ? ~0ull : 0ull;
+  }
+  __device__ float count() const {
+    if (FULL) return (float)EPT;
+    int n = 0;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) d[v * VEC + i] = 0.f;
+    for (int v = 0; v < N * VC; ++v) n += pl.on(v) ? VEC : 0;
+    return (float)n;
+  }
+  __device__ void load(const T* row, int k, Part& p) const {
+#pragma unroll
+    for (int j = 0; j < VC; ++j) p.v[j] = __ldcs(reinterpret_cast<const R*>(row) + pl.at(VC * k + j));
+  }
+  template <typename Rg> __device__ void get(const Rg& ring, int st, int k, const T* row, uint64_t (&d)[NP]) const {
+    Part p;
+#pragma unroll
+    for (int j = 0; j < VC; ++j) p.v[j] = ring.get(st, VC * k + j, row);
+    pairs(p, d);
+  }
+  static __device__ void pairs(const Part& p, uint64_t (&d)[NP]) {
+    float f[CE];
+#pragma unroll
+    for (int j = 0; j < VC; ++j) unpack(p.v[j], f + j);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) d[i] = f2(f[2 * i], f[2 * i + 1]);
+  }
+  // rounded once and written past the caches (nothing here reads it again)
+  __device__ void put(T* row, int k, const uint64_t (&d)[NP]) const {
+    float f[CE];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) uf2(d[i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < VC; ++j) {
+      R pk;
+      pack(f + j, pk);
+      if (pl.on(VC * k + j)) __stcs(reinterpret_cast<R*>(row) + pl.first + 32 * (VC * k + j), pk);
+    }
+  }
+  // column of element i (existing chunks only)
+  __device__ int col(int k, int i) const {
+    return VEC == 1 ? pl.first + 32 * (2 * k + i) : (pl.first + 32 * k) * VEC + i;
+  }
+  __device__ bool on(int k, int i) const { return pl.on(VEC == 1 ? 2 * k + i : k); }
+  // gain or bias of chunk k (null: `none`), `add` added
+  __device__ void affine(const float* p, float none, float add, int k, uint64_t (&d)[NP]) const {
+    float f[CE];
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < CE; ++i) f[i] = none;
+    } else if constexpr (VEC % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < CE; i += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p + pl.at(k) * VEC + i));
+        f[i] = q.x;
+        f[i + 1] = q.y;
+        f[i + 2] = q.z;
+        f[i + 3] = q.w;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CE; ++i) f[i] = __ldg(p + (VEC == 1 ? pl.at(2 * k + i) : pl.at(k) * VEC + i));
     }
-    if (r + teams < rg.r1) load_row<T, VEC>(x + (r + teams) * a.x_stride, nvec, t, team, nx);
-    const long long g = r / a.rows_per_group;
-    if (g != cur_g) {
-      load_affine<VEC>(a.w, 1.f, a.gain_one, g, a.C, nvec, t, team, w);
-      load_affine<VEC>(a.b, 0.f, 0.f, g, a.C, nvec, t, team, b);
-      cur_g = g;
+    if (!p) add = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) d[i] = add2(f2(f[2 * i], f[2 * i + 1]), both(add));
+  }
+};
+
+// Warps of a backward block: 96 registers a thread with wide vectors (20 warps;
+// 15 of 32 elements a thread took 283 us where 20 of 16 take 195), 128 with
+// narrow ones, which spill below that.
+template <int VEC> __host__ __device__ constexpr int bwd_warps() { return VEC >= 4 ? 20 : 16; }
+
+// First byte behind the rings of the teams.
+__host__ __device__ constexpr int ring_end(int bytes) { return (bytes + 15) & ~15; }
+
+// RW rows of one group per team.  Block b holds the teams b TEAMS ..; a team's
+// rows are rows RW k .. of its group.
+template <typename T, int VEC, int EPT, int RW, bool FULL>
+__global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT == 32 ? 2 : 1)
+    norm_fwd_kernel(const NormArgs a, const T* x, T* y) {
+  using Ch = Chunks<T, VEC, EPT, FULL>;
+  constexpr int N = Ch::N, NP = Ch::NP;
+  __shared__ float2 red[RW][MAX_WARPS];
+  __shared__ float red_n[MAX_WARPS];
+  const Lane L(a.warps);
+  const Ch ch{{(L.t >> 5) * (32 * EPT / VEC) + L.lane, a.C / VEC}};
+  const unsigned per_group = (unsigned)((a.rows_per_group + RW - 1) / RW);
+  unsigned unit = blockIdx.x * L.teams + L.id, g = blockIdx.y;
+  if (a.flat) {                      // many short groups: numbered through
+    g = unit / per_group;
+    unit -= g * per_group;
+  }
+  if (g >= (unsigned)a.groups || unit >= per_group) return;   // whole teams: the others meet on barriers of their own
+  const long long in_group = (long long)unit * RW;
+  const float inv_c = a.inv_c;
+  const long long r0 = g * a.rows_per_group + in_group;
+  bool on[RW];
+#pragma unroll
+  for (int k = 0; k < RW; ++k) on[k] = in_group + k < a.rows_per_group;
+  uint64_t d[RW][N * NP];            // x - x0
+  float x0[RW], s[RW], m2[RW], m_t[RW];
+  {
+    typename Ch::Part raw[RW][N];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const T* row = x + (on[k] ? r0 + k : r0) * a.x_stride;
+      x0[k] = to_f(row[0]);
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        ch.load(row, c, raw[k][c]);
     }
+    const float n_t = ch.count(), inv_t = FULL ? 1.f / EPT : n_t > 0.f ? 1.f / n_t : 0.f;
+    const float n_w = FULL ? 32.f * EPT : warp_sum(n_t), inv_w = FULL ? 1.f / (32 * EPT) : n_w > 0.f ? 1.f / n_w : 0.f;
+    if (L.lane == 0) red_n[L.warp] = n_w;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) s += d[i];
-    team_sum2(s, s1, red[0], warps, warp, lane);
-    const float m0 = s * inv_c;
-    s1 = 0.f;
+    for (int k = 0; k < RW; ++k) {
+      uint64_t s2[2] = {0ull, 0ull}, q2[2] = {0ull, 0ull};
+      const uint64_t X0 = both(x0[k]);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (v * team + t < nvec) {
+      for (int c = 0; c < N; ++c) {
+        uint64_t p[NP];
+        ch.pairs(raw[k][c], p);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float e = d[v * VEC + i] - m0;
-          d[v * VEC + i] = e;
-          s1 += e;
-          s2 = fmaf(e, e, s2);
+        for (int i = 0; i < NP; ++i) {
+          d[k][c * NP + i] = sub2(p[i], X0) & ch.mask(c);
+          s2[i & 1] = add2(s2[i & 1], d[k][c * NP + i]);
         }
       }
-    team_sum2(s1, s2, red[1], warps, warp, lane);
-    // the rounding of the first mean, put right by the mean of the differences
-    const float dm = s1 * inv_c;
-    const float var = fmaxf(s2 * inv_c - dm * dm, 0.f) + (s2 != s2 ? s2 : 0.f);
-    const float rstd = 1.f / sqrtf(var + a.eps);
-    T* yr = y + r * a.y_stride;
+      s[k] = sum2(add2(s2[0], s2[1]));
+      m_t[k] = s[k] * inv_t;
+      const uint64_t M = both(m_t[k]);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (v * team + t < nvec) {
-        float o[VEC];
+      for (int c = 0; c < N; ++c) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = fmaf((d[v * VEC + i] - dm) * rstd, w[v * VEC + i], b[v * VEC + i]);
-        R pk;
-        pack(o, pk);
-        __stcs(reinterpret_cast<R*>(yr) + v * team + t, pk);
+        for (int i = 0; i < NP; ++i) {
+          const uint64_t e = sub2(d[k][c * NP + i], M) & ch.mask(c);
+          q2[i & 1] = fma2(e, e, q2[i & 1]);
+        }
       }
-    if (t == 0) {
-      if (a.mean_out) a.mean_out[r] = m0 + dm;
-      if (a.rstd_out) a.rstd_out[r] = rstd;
+      m2[k] = sum2(add2(q2[0], q2[1]));
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) s[k] = warp_sum(s[k]);
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const float dw = m_t[k] - s[k] * inv_w;
+      m2[k] = warp_sum(fmaf(n_t * dw, dw, m2[k]));
+    }
+    if (L.warps > 1) {
+      if (L.lane == 0) {
+#pragma unroll
+        for (int k = 0; k < RW; ++k) red[k][L.warp] = make_float2(s[k] * inv_w, m2[k]);
+      }
+      team_sync(L.warps, L.id);
+      const float2(*rd)[MAX_WARPS] = red;
+#pragma unroll
+      for (int k = 0; k < RW; ++k) s[k] = m2[k] = 0.f;
+      for (int i = L.id * L.warps; i < (L.id + 1) * L.warps; ++i)
+#pragma unroll
+        for (int k = 0; k < RW; ++k) s[k] = fmaf(FULL ? 32.f * EPT : red_n[i], rd[k][i].x, s[k]);
+      for (int i = L.id * L.warps; i < (L.id + 1) * L.warps; ++i)
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+          const float dm = rd[k][i].x - s[k] * inv_c;
+          m2[k] += fmaf((FULL ? 32.f * EPT : red_n[i]) * dm, dm, rd[k][i].y);
+        }
+    }
+  }
+  uint64_t RS[RW], MR[RW];
+#pragma unroll
+  for (int k = 0; k < RW; ++k) {
+    const float mean = s[k] * inv_c;             // of x - x0
+    const float rstd = rsqrtf(fmaf(m2[k], inv_c, a.eps));
+    RS[k] = both(rstd);
+    MR[k] = both(-mean * rstd);
+    if (L.t == 0 && on[k]) {
+      if (a.mean_out) a.mean_out[r0 + k] = x0[k] + mean;
+      if (a.rstd_out) a.rstd_out[r0 + k] = rstd;
+    }
+  }
+  const float *gw = a.w ? a.w + (long long)g * a.C : nullptr, *gb = a.b ? a.b + (long long)g * a.C : nullptr;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    uint64_t w[NP], b[NP], o[NP];
+    ch.affine(gw, 1.f, a.gain_one, c, w);
+    ch.affine(gb, 0.f, 0.f, c, b);
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) o[i] = fma2(fma2(d[k][c * NP + i], RS[k], MR[k]), w[i], b[i]);
+      if (on[k]) ch.put(y + (r0 + k) * a.y_stride, c, o);
     }
   }
 }
 
-// dx of the block's rows and the block's column sums per group.  With
-// one-warp teams the block's warps interleave their rows and add their sums
-// in shared memory, in warp order, when a group ends.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(32 * MAX_WARPS)
-    norm_bwd_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ dy, T* __restrict__ dx) {
-  using R = typename Raw<T, VEC>::type;
-  constexpr int NV = EPT / VEC;
-  __shared__ float red[2][2][MAX_WARPS];
-  __shared__ float comb[EPT * 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = a.warps, team = warps * 32, teams = (int)blockDim.x / team;
-  const int t = warps == 1 ? lane : (int)threadIdx.x;
-  const int nvec = a.C / VEC;
+// dx of the block's rows and the block's column sums per group.  The second
+// pass over a row reads the ring again: the sums take the registers.  There
+// dx = rstd gy + x A + B with A = -rstd^2 c2, B = rstd^2 c2 mean - rstd c1
+// (c1, c2 the two row means), whose rounding is that of the saved mean.
+template <typename T, int VEC, int EPT, bool FULL>
+__global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
+    norm_bwd_kernel(const NormArgs a, const T* x, const T* dy, T* dx) {
+  using Rg = Ring<T, VEC, EPT, FULL>;
+  using Ch = Chunks<T, VEC, EPT, FULL>;
+  constexpr int N = Ch::N, NP = Ch::NP, CE = Ch::CE, STAGES = Rg::STAGES;
+  extern __shared__ __align__(16) unsigned char ring_smem[];
+  __shared__ float2 red[2][MAX_WARPS];
+  const Lane L(a.warps);
+  const int team = L.team, t = L.t;
+  const Place<FULL> pl{(t >> 5) * (32 * EPT / VEC) + L.lane, a.C / VEC};
+  unsigned char* base = ring_smem + L.id * 2 * STAGES * Rg::bytes(L.team);
+  const Rg rx{base, pl, team, t, a.C}, ry{base + STAGES * Rg::bytes(L.team), pl, team, t, a.C};
+  const Ch ch{pl};
+  // sums over the teams: [EPT][team]
+  float* sw = reinterpret_cast<float*>(ring_smem + ring_end(L.teams * 2 * STAGES * Rg::bytes(L.team)));
   const float inv_c = 1.f / (float)a.C;
   const Range rg = block_rows(a);
   const bool sums = a.partial != nullptr;
-  int par = 0;
+  const long long first = rg.r0 + L.id;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) {
+    if (first + s * L.teams < rg.r1) {
+      rx.fetch(s, x + (first + s * L.teams) * a.x_stride);
+      ry.fetch(s, dy + (first + s * L.teams) * a.y_stride);
+    }
+    copy_commit();
+  }
+  float next_mean = 0.f, next_rstd = 0.f;
+  if (first < rg.r1) {
+    next_mean = a.mean[first];
+    next_rstd = a.rstd[first];
+  }
+  int st = 0, par = 0;
+  long long r = first;
   for (long long s0 = rg.r0; s0 < rg.r1;) {       // the block's rows of one group
     const long long g = s0 / a.rows_per_group;
     long long s1 = (g + 1) * a.rows_per_group;
     if (s1 > rg.r1) s1 = rg.r1;
-    float w[EPT], aw[EPT], ab[EPT];
-    load_affine<VEC>(a.w, 1.f, a.gain_one, g, a.C, nvec, t, team, w);
+    uint64_t w[N][NP], aw[N * NP], ab[N * NP];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) aw[i] = ab[i] = 0.f;
-    R nx[NV], ny[NV];
-    long long r = s0 + (teams > 1 ? warp : 0);
-    float nm = 0.f, nr = 0.f;
-    if (r < s1) {
-      load_row<T, VEC>(x + r * a.x_stride, nvec, t, team, nx);
-      load_row<T, VEC>(dy + r * a.y_stride, nvec, t, team, ny);
-      nm = a.mean[r];
-      nr = a.rstd[r];
-    }
-    for (; r < s1; r += teams) {
-      const float mean = nm, rstd = nr;
-      float xh[EPT], gy[EPT];
-      float c1 = 0.f, c2 = 0.f;
+    for (int k = 0; k < N; ++k)
+      ch.affine(a.w ? a.w + g * a.C : nullptr, 1.f, a.gain_one, k, w[k]);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (v * team + t < nvec) {
-          unpack(nx[v], xh + v * VEC);
-          unpack(ny[v], gy + v * VEC);
+    for (int i = 0; i < N * NP; ++i) aw[i] = ab[i] = 0ull;
+    for (; r < s1; r += L.teams) {
+      const T *xr = x + r * a.x_stride, *yr = dy + r * a.y_stride;
+      if constexpr (Rg::WORDS) {
+        copy_wait<STAGES - 2>();
+        team_sync(L.warps, L.id);    // the rows are whole, and the stage fetched below is read by nobody
+      }
+      const long long ahead = r + (long long)(STAGES - 1) * L.teams;
+      if (ahead < rg.r1) {
+        const int sn = st == 0 ? STAGES - 1 : st - 1;
+        rx.fetch(sn, x + ahead * a.x_stride);
+        ry.fetch(sn, dy + ahead * a.y_stride);
+      }
+      copy_commit();
+      const float mean = next_mean, rstd = next_rstd;
+      if (r + L.teams < rg.r1) {
+        next_mean = a.mean[r + L.teams];
+        next_rstd = a.rstd[r + L.teams];
+      }
+      if constexpr (!Rg::WORDS) copy_wait<STAGES - 1>();
+      uint64_t C1 = 0ull, C2 = 0ull;
+      const uint64_t RS = both(rstd), MR = both(-mean * rstd);
 #pragma unroll
-          for (int i = v * VEC; i < (v + 1) * VEC; ++i) {
-            xh[i] = (xh[i] - mean) * rstd;
-            aw[i] = fmaf(gy[i], xh[i], aw[i]);
-            ab[i] += gy[i];
-            gy[i] *= w[i];
-            c1 += gy[i];
-            c2 = fmaf(gy[i], xh[i], c2);
+      for (int k = 0; k < N; ++k) {
+          uint64_t xv[NP], gv[NP];
+          ch.get(rx, st, k, xr, xv);
+          ch.get(ry, st, k, yr, gv);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            gv[i] &= ch.mask(k);                    // an absent element adds nothing
+            const uint64_t xh = fma2(xv[i], RS, MR);
+            aw[k * NP + i] = fma2(gv[i], xh, aw[k * NP + i]);
+            ab[k * NP + i] = add2(ab[k * NP + i], gv[i]);
+            const uint64_t gy = mul2(gv[i], w[k][i]);
+            C1 = add2(C1, gy);
+            C2 = fma2(gy, xh, C2);
           }
         }
-      }
-      if (r + teams < s1) {
-        load_row<T, VEC>(x + (r + teams) * a.x_stride, nvec, t, team, nx);
-        load_row<T, VEC>(dy + (r + teams) * a.y_stride, nvec, t, team, ny);
-        nm = a.mean[r + teams];
-        nr = a.rstd[r + teams];
-      }
       if (dx) {
-        team_sum2(c1, c2, red[par], warps, warp, lane);
-        par ^= 1;
-        c1 *= inv_c;
-        c2 *= inv_c;
+        float c1 = warp_sum(sum2(C1)), c2 = warp_sum(sum2(C2));
+        if (L.warps > 1) {
+          if (L.lane == 0) red[par][L.warp] = make_float2(c1, c2);
+          team_sync(L.warps, L.id);
+          const float2 p = L.lane < L.warps ? red[par][L.id * L.warps + L.lane] : make_float2(0.f, 0.f);
+          c1 = warp_sum(p.x);
+          c2 = warp_sum(p.y);
+          par ^= 1;
+        }
+        const float A = -rstd * rstd * (c2 * inv_c);
+        const uint64_t KA = both(A), KB = both(fmaf(-A, mean, -rstd * (c1 * inv_c)));
         T* dr = dx + r * a.x_stride;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-          if (v * team + t < nvec) {
-            float o[VEC];
+        for (int k = 0; k < N; ++k) {
+            uint64_t xv[NP], gv[NP];
+            ch.get(rx, st, k, xr, xv);
+            ch.get(ry, st, k, yr, gv);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = rstd * (gy[v * VEC + i] - fmaf(xh[v * VEC + i], c2, c1));
-            R pk;
-            pack(o, pk);
-            __stcs(reinterpret_cast<R*>(dr) + v * team + t, pk);
+            for (int i = 0; i < NP; ++i) xv[i] = fma2(mul2(gv[i], w[k][i]), RS, fma2(xv[i], KA, KB));
+            ch.put(dr, k, xv);
           }
       }
+      st = st == STAGES - 1 ? 0 : st + 1;
     }
     if (sums) {
       float* out = a.partial + ((long long)blockIdx.x + g) * 2 * a.C;
-      if (teams > 1) {
-        for (int h = 0; h < 2; ++h) {
-          for (int k = 0; k < teams; ++k) {
-            if (warp == k) {
 #pragma unroll
-              for (int i = 0; i < EPT; ++i) {
-                const float v = h ? ab[i] : aw[i];
-                comb[i * 32 + lane] = k == 0 ? v : comb[i * 32 + lane] + v;
+      for (int h = 0; h < 2; ++h, out += a.C) {
+        for (int id = 0; id < L.teams; ++id) {    // over the teams, in order
+          if (L.id == id) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              float f[CE];
+#pragma unroll
+              for (int i = 0; i < NP; ++i) uf2(h ? ab[k * NP + i] : aw[k * NP + i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+              for (int i = 0; i < CE; ++i) {
+                float* c = sw + (k * CE + i) * team + t;
+                if (id > 0) f[i] += *c;
+                if (id < L.teams - 1)
+                  *c = f[i];
+                else if (ch.on(k, i))
+                  out[ch.col(k, i)] = f[i];
               }
             }
-            __syncthreads();
           }
-          if (warp == 0) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-              if (v * 32 + lane < nvec) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                  out[(long long)h * a.C + (v * 32 + lane) * VEC + i] = comb[(v * VEC + i) * 32 + lane];
-              }
-          }
-          __syncthreads();
+          if (L.teams > 1) __syncthreads();
         }
-      } else {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          if (v * team + t < nvec) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              out[(v * team + t) * VEC + i] = aw[v * VEC + i];
-              out[(long long)a.C + (v * team + t) * VEC + i] = ab[v * VEC + i];
-            }
-          }
       }
     }
     s0 = s1;
@@ -360,8 +589,6 @@ __device__ inline void block_sum2(float& a, float& b, float (*red)[32]) {
     b += red[1][i];
   }
 }
-__device__ inline float to_f(float v) { return v; }
-__device__ inline float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ inline void from_f(float v, float* p) { *p = v; }
 __device__ inline void from_f(float v, __nv_bfloat16* p) { *p = __float2bfloat16(v); }
 
@@ -452,44 +679,37 @@ __global__ void __launch_bounds__(256)
 // Largest vector (elements) that divides the row and both row strides.
 template <typename T>
 int vec_of(const NormArgs& a) {
-  const int opts_b[3] = {8, 2, 1}, opts_f[3] = {4, 1, 1};
-  for (int i = 0; i < 3; ++i) {
+  const int opts_b[4] = {8, 4, 2, 1}, opts_f[4] = {4, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
     const int v = sizeof(T) == 2 ? opts_b[i] : opts_f[i];
     if (a.C % v == 0 && a.x_stride % v == 0 && a.y_stride % v == 0) return v;
   }
   return 1;
 }
 
-// Warps of a row's team and the block's threads.
-inline void team_of(NormArgs& a, int vec, int* threads) {
-  const int nvec = a.C / vec;
-  const int per = 32 * (EPT / vec);
-  a.warps = (nvec + per - 1) / per;
-  *threads = a.warps == 1 ? 32 * TEAMS1 : 32 * a.warps;
+// 8 elements a thread when the SMs hold all rows at once like that.
+inline bool few_rows(long long rows, int C, int num_sms) { return rows * ((C + 255) / 256) <= (long long)num_sms * 32; }
+
+template <typename T, int VEC, int EPT, int RW>
+cudaError_t fwd_v(NormArgs a, const T* x, T* y, cudaStream_t s) {
+  a.warps = (a.C + 32 * EPT - 1) / (32 * EPT);
+  auto kernel = a.C == 32 * EPT * a.warps ? norm_fwd_kernel<T, VEC, EPT, RW, true> : norm_fwd_kernel<T, VEC, EPT, RW, false>;
+  const int teams = a.warps < 4 ? 4 / a.warps : 1;       // blocks of three warps or more
+  const long long per_group = (a.rows_per_group + RW - 1) / RW;
+  a.flat = a.groups > 65535 || per_group < 8 * teams;
+  const long long units = a.flat ? per_group * a.groups : per_group;
+  const dim3 grid((unsigned)((units + teams - 1) / teams), a.flat ? 1 : a.groups);
+  kernel<<<grid, teams * 32 * a.warps, 0, s>>>(a, x, y);
+  return cudaGetLastError();
 }
 
-template <typename K>
-cudaError_t resident_blocks(K kernel, int threads, int num_sms, long long* blocks) {
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-  *blocks = (long long)num_sms * (per_sm < 1 ? 1 : per_sm);
-  return e;
-}
+// Elements a thread of the long forms: narrow vectors cost an address each,
+// and 32 of them spill.
+template <int VEC> constexpr int long_ept() { return VEC >= 4 ? 32 : 16; }
 
 template <typename T, int VEC>
-cudaError_t fwd_v(NormArgs a, const T* x, T* y, int num_sms, cudaStream_t s) {
-  int threads;
-  team_of(a, VEC, &threads);
-  long long blocks;
-  cudaError_t e = resident_blocks(norm_fwd_kernel<T, VEC>, threads, num_sms, &blocks);
-  if (e != cudaSuccess) return e;
-  const long long teams = a.warps == 1 ? TEAMS1 : 1;
-  const long long most = (a.rows + teams - 1) / teams;
-  if (blocks > most) blocks = most;
-  a.rows_per_block = (a.rows + blocks - 1) / blocks;
-  blocks = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
-  norm_fwd_kernel<T, VEC><<<(unsigned)blocks, threads, 0, s>>>(a, x, y);
-  return cudaGetLastError();
+cudaError_t fwd_e(const NormArgs& a, const T* x, T* y, int num_sms, cudaStream_t s) {
+  return few_rows(a.rows, a.C, num_sms) ? fwd_v<T, VEC, 8, 1>(a, x, y, s) : fwd_v<T, VEC, long_ept<VEC>(), 2>(a, x, y, s);
 }
 
 template <typename T>
@@ -503,20 +723,29 @@ cudaError_t fwd_t(const NormArgs& a, const void* x, void* y, int num_sms, cudaSt
   }
   const int v = vec_of<T>(a);
   if constexpr (sizeof(T) == 2) {
-    if (v == 8) return fwd_v<T, 8>(a, xp, yp, num_sms, s);
-    if (v == 2) return fwd_v<T, 2>(a, xp, yp, num_sms, s);
+    if (v >= 4) return fwd_e<T, 4>(a, xp, yp, num_sms, s);
+    if (v == 2) return fwd_e<T, 2>(a, xp, yp, num_sms, s);
   } else {
-    if (v == 4) return fwd_v<T, 4>(a, xp, yp, num_sms, s);
+    if (v == 4) return fwd_e<T, 4>(a, xp, yp, num_sms, s);
   }
-  return fwd_v<T, 1>(a, xp, yp, num_sms, s);
+  return fwd_e<T, 1>(a, xp, yp, num_sms, s);
 }
 
 template <typename T, int VEC>
 cudaError_t bwd_v(NormArgs a, const T* x, const T* dy, T* dx, cudaStream_t s) {
-  int threads;
-  team_of(a, VEC, &threads);
+  constexpr int EPT = 16, WARPS = bwd_warps<VEC>();
+  using Rg = Ring<T, VEC, EPT, true>;
+  a.warps = (a.C + 32 * EPT - 1) / (32 * EPT);
+  auto kernel = a.C == 32 * EPT * a.warps ? norm_bwd_kernel<T, VEC, EPT, true> : norm_bwd_kernel<T, VEC, EPT, false>;
+  // as many teams as the warps allow, as many as the shared memory takes, one block an SM
+  int teams = WARPS / a.warps < MAX_TEAMS ? WARPS / a.warps : MAX_TEAMS;
+  auto bytes = [&](int n) { return ring_end(n * 2 * Rg::STAGES * Rg::bytes(32 * a.warps)) + (n > 1 ? 4 * EPT * 32 * a.warps : 0); };
+  while (teams > 1 && bytes(teams) > 220 * 1024) --teams;
+  const int smem = bytes(teams);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   const long long blocks = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
-  norm_bwd_kernel<T, VEC><<<(unsigned)blocks, threads, 0, s>>>(a, x, dy, dx);
+  kernel<<<(unsigned)blocks, teams * 32 * a.warps, smem, s>>>(a, x, dy, dx);
   return cudaGetLastError();
 }
 
@@ -541,6 +770,7 @@ cudaError_t bwd_t(const NormArgs& a, const void* x, const void* dy, void* dx, in
   const int v = vec_of<T>(a);
   if constexpr (sizeof(T) == 2) {
     if (v == 8) return bwd_v<T, 8>(a, xp, gp, dp, s);
+    if (v == 4) return bwd_v<T, 4>(a, xp, gp, dp, s);
     if (v == 2) return bwd_v<T, 2>(a, xp, gp, dp, s);
   } else {
     if (v == 4) return bwd_v<T, 4>(a, xp, gp, dp, s);
@@ -550,11 +780,7 @@ cudaError_t bwd_t(const NormArgs& a, const void* x, const void* dy, void* dx, in
 
 }  // namespace ln
 
-long long norm_bwd_blocks(long long rows, int C) {
-  const long long teams = C <= ln::EPT * 32 ? ln::TEAMS1 : 1;
-  const long long most = (rows + teams - 1) / teams;
-  return most < kNormBlocks ? most : kNormBlocks;
-}
+long long norm_bwd_blocks(long long rows) { return rows < kNormBlocks ? rows : kNormBlocks; }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const void* x, void* y, int num_sms, cudaStream_t s) {
   return dtype == FVATTN_BF16 ? ln::fwd_t<__nv_bfloat16>(a, x, y, num_sms, s) : ln::fwd_t<float>(a, x, y, num_sms, s);

@@ -444,35 +444,49 @@ def qkv_rope(shape: Shape, x, w, ws, bias=None, rope: Optional[Rope] = None, t_o
     return q, k, v
 
 
-@contextlib.contextmanager
-def _launch(tensors, stream: Optional[torch.cuda.Stream]):
-    """The tensors' device made current, with the stream to launch on (the
-    given one, or the device's current one; new outputs belong to it)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("expected every tensor on one device")
-    if stream is not None and stream.device != dev:
-        raise ValueError("the stream belongs to another device than the tensors")
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        with torch.cuda.stream(s):
-            yield ctypes.c_void_p(s.cuda_stream)
+class _Launch:
+    """Makes the tensors' device current and picks the stream to launch on
+    (the given one, or the device's current one; new outputs belong to it).
+    Does nothing more than read the stream when that is already so."""
+    __slots__ = ("dev", "stream", "guards")
+
+    def __init__(self, tensors, stream: Optional[torch.cuda.Stream]):
+        dev = -2
+        for t in tensors:
+            if t is None:
+                continue
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("expected a CUDA tensor")
+            if i != dev:
+                if dev != -2:
+                    raise ValueError("expected every tensor on one device")
+                dev = i
+        if stream is not None and stream.device.index != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.dev, self.stream, self.guards = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is None and torch.cuda.current_device() == self.dev:
+            return torch.cuda.current_stream(self.dev).cuda_stream
+        self.guards = contextlib.ExitStack()
+        self.guards.enter_context(torch.cuda.device(self.dev))
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
+        self.guards.enter_context(torch.cuda.stream(s))
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guards is not None:
+            self.guards.close()
 
 
 def _typed(t: Optional[torch.Tensor], dtype, shape, what: str):
     """Pointer of a contiguous tensor of this dtype and shape (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _torch_dtype(dtype: int):
@@ -507,7 +521,7 @@ def _rows(t: Optional[torch.Tensor], norm: Norm, stride: int, what: str):
     if not ok:
         raise ValueError(f"{what}: expected {norm.rows} {_torch_dtype(norm.dtype)} rows of {norm.channels} "
                          f"with row stride {stride}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
@@ -522,7 +536,7 @@ def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rst
     """Layer norm of the rows of x ([..., channels]) with weight and bias
     [groups, channels] float32 (or None): returns (y, mean, rstd)."""
     affine = (norm.groups, norm.channels)
-    with _launch((x, weight, bias, y, mean, rstd), stream) as s:
+    with _Launch((x, weight, bias, y, mean, rstd), stream) as s:
         px = _rows(x, norm, norm.x_stride, "x")
         if y is None:
             y = _new_rows(x, norm, norm.y_stride)
@@ -543,7 +557,7 @@ def layer_norm_bwd(norm: Norm, x, dy, mean, rstd, ws, weight=None, grads=None, s
     """Backward of layer_norm_fwd: returns (dx, dweight, dbias).  grads: the
     three output tensors, None for a gradient that is not wanted."""
     affine = (norm.groups, norm.channels)
-    with _launch((x, dy, mean, rstd, ws, weight, *(grads or ())), stream) as s:
+    with _Launch((x, dy, mean, rstd, ws, weight, *(grads or ())), stream) as s:
         if grads is None:
             grads = (_new_rows(x, norm, norm.x_stride),
                      torch.empty(affine, dtype=torch.float32, device=x.device),
@@ -569,7 +583,7 @@ def make_window(batch, heads, head_dim, q_len, kv_len, window, sinks=0, unit=1, 
                   int(kv_len), int(unit), int(window), int(sinks), dtype, float(scale))
 
 
-def window_workspace(win: Window, device="cuda") -> torch.Tensor:
+def window_workspace(win: Window, backward=False, device="cuda") -> torch.Tensor:
     """A device workspace for window_fwd (caller-owned)."""
     n = ctypes.c_size_t()
     _check("fvattn_workspace_size_window", lib().fvattn_workspace_size_window(ctypes.byref(win), ctypes.byref(n)))
@@ -577,22 +591,20 @@ def window_workspace(win: Window, device="cuda") -> torch.Tensor:
 
 
 def _view(t: torch.Tensor, batch: int, heads: int, tokens: int, d: int, what: str):
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (batch, heads, tokens, d) or (t.numel() and t.stride(3) != 1):
+    sb, sh, st, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if t.dtype != torch.bfloat16 or t.shape != (batch, heads, tokens, d) or (sd != 1 and t.numel()):
         raise ValueError(f"{what}: expected a bfloat16 tensor [{batch}, {heads}, {tokens}, {d}] with contiguous rows")
-    return ctypes.byref(View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+    return ctypes.byref(View(t.data_ptr(), sb, sh, st))
 
 
 def _new_heads(like: torch.Tensor, lens):
     """An output shaped and laid out like `like`; rows behind a sequence's
     length are not written by the library, so with lengths they start as 0."""
-    new = torch.empty_strided if lens is None else _zeros_strided
-    dense = like.is_contiguous() or like.transpose(1, 2).is_contiguous()
-    strides = like.stride() if dense else torch.empty(like.shape, device="meta").stride()
-    return new(like.shape, strides, dtype=like.dtype, device=like.device)
-
-
-def _zeros_strided(shape, strides, dtype, device):
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device).zero_()
+    if like.is_contiguous() or not like.transpose(1, 2).is_contiguous():
+        new = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    else:                                               # token-major
+        new = torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
+    return new if lens is None else new.zero_()
 
 
 def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, lse=None, stream=None):
@@ -600,7 +612,7 @@ def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, ls
     [B, kv_heads, kv_len, d] (any strides with contiguous rows): returns
     (out, lse).  q_lens, kv_lens: int32 device tensors [B] or None."""
     B, H, Hk, D = win.batch, win.heads, win.kv_heads, win.head_dim
-    with _launch((q, k, v, ws, q_lens, kv_lens, out, lse), stream) as s:
+    with _Launch((q, k, v, ws, q_lens, kv_lens, out, lse), stream) as s:
         vq = _view(q, B, H, win.q_len, D, "q")
         if out is None:
             out = _new_heads(q, q_lens)
