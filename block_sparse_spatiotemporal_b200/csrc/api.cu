@@ -773,6 +773,14 @@ WinWs win_ws(const WinFwdArgs& a) {
   return L;
 }
 
+struct WinBwdWs {
+  size_t lse2, dd, total;
+};
+WinBwdWs win_bwd_ws(const WinGeom& g) {
+  const size_t rows = align_up(sizeof(float) * (size_t)g.B * g.H * g.Nq);
+  return WinBwdWs{kAlign, kAlign + rows, kAlign + 2 * rows};
+}
+
 }  // namespace
 
 extern "C" {
@@ -1274,6 +1282,87 @@ int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvat
   StageTimer t(FVATTN_STAGE_WINDOW, s);
   FV_CUDA(launch_window_fwd(mq, mk, mv, a, dev.sms, s));
   t.kernels = 1;
+  return FVATTN_OK;
+}
+
+int fvattn_workspace_size_window_bwd(const fvattn_window* win, size_t* bytes) {
+  if (!bytes) return FVATTN_ERR_INVALID_ARG;
+  WinGeom g;
+  FV_TRY(win_geom(win, &g));
+  *bytes = win_bwd_ws(g).total;
+  return FVATTN_OK;
+}
+
+int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvattn_view* k, const fvattn_view* v,
+                      const fvattn_view* out, const fvattn_view* dout, const float* lse, const int32_t* q_lens,
+                      const int32_t* kv_lens, const fvattn_view* dq, const fvattn_view* dk, const fvattn_view* dv,
+                      void* ws, size_t ws_bytes, fvattn_stream_t stream) {
+  WinGeom g;
+  FV_TRY(win_geom(win, &g));
+  for (const fvattn_view* t : {q, out, dout}) FV_TRY(check_view(t, g, g.H, g.Nq, false));
+  for (const fvattn_view* t : {k, v}) FV_TRY(check_view(t, g, g.Hk, g.Nk, false));
+  FV_TRY(check_view(dq, g, g.H, g.Nq, true));
+  for (const fvattn_view* t : {dk, dv}) FV_TRY(check_view(t, g, g.Hk, g.Nk, true));
+  if ((g.Nq > 0 && !lse) || !aligned(lse, 4) || !aligned(q_lens, 4) || !aligned(kv_lens, 4))
+    return FVATTN_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign)) return FVATTN_ERR_INVALID_ARG;
+  const int q_tiles = (g.Nq + 127) / 128, k_tiles = (g.Nk + 127) / 128;
+  if ((int64_t)g.B * g.H * q_tiles > (1 << 28) || (int64_t)g.B * g.Hk * k_tiles > (1 << 28)) return FVATTN_ERR_SHAPE;
+  g.q_lens = q_lens;
+  g.kv_lens = kv_lens;
+  const WinBwdWs L = win_bwd_ws(g);
+  if (ws_bytes < L.total) return FVATTN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  FV_TRY(device_info(&dev));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  FV_CUDA(cudaMemsetAsync(base, 0, sizeof(int), s));
+  if (g.Nq == 0 && g.Nk == 0) return FVATTN_OK;
+  // a tensor without rows has no address: its maps, which no load uses, take another's
+  const void* any = g.Nq > 0 ? q->data : k->data;
+  float* lse2 = reinterpret_cast<float*>(base + L.lse2);
+  float* dd = reinterpret_cast<float*>(base + L.dd);
+  const WinOut wo{out->data, out->batch, out->head, out->token}, wd{dout->data, dout->batch, dout->head, dout->token};
+  if (g.Nq > 0) {
+    StageTimer t(FVATTN_STAGE_WINDOW_PREP, s);
+    FV_CUDA(launch_window_prep(g, wo, wd, lse, lse2, dd, s));
+    t.kernels = 1;
+  }
+  WinBwdArgs a{};
+  a.g = g;
+  a.lse2 = lse2;
+  a.dd = dd;
+  a.status = reinterpret_cast<int*>(base);
+  a.wait_cap = kDefaultWaitCap;
+  CUtensorMap m0, m1, m2, m3;
+  if (g.Nk > 0) {
+    FV_TRY(make_head_map(&m0, *k, g, g.Hk, g.Nk, 128, any));
+    FV_TRY(make_head_map(&m1, *v, g, g.Hk, g.Nk, 128, any));
+    FV_TRY(make_head_map(&m2, *q, g, g.H, g.Nq, 64, any));
+    FV_TRY(make_head_map(&m3, *dout, g, g.H, g.Nq, 64, any));
+    a.tiles = k_tiles;
+    a.n_items = g.B * g.Hk * k_tiles;
+    const int64_t sink_tiles = g.window > 0 ? ((int64_t)g.sinks * g.unit + 127) / 128 : 0;
+    a.heavy_tiles = (int)(sink_tiles < k_tiles ? sink_tiles : k_tiles);
+    a.out0 = WinOut{dk->data, dk->batch, dk->head, dk->token};
+    a.out1 = WinOut{dv->data, dv->batch, dv->head, dv->token};
+    StageTimer t(FVATTN_STAGE_WINDOW_KV, s);
+    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, true, dev.sms, s));
+    t.kernels = 1;
+  }
+  if (g.Nq > 0) {
+    FV_TRY(make_head_map(&m0, *q, g, g.H, g.Nq, 128, any));
+    FV_TRY(make_head_map(&m1, *dout, g, g.H, g.Nq, 128, any));
+    FV_TRY(make_head_map(&m2, *k, g, g.Hk, g.Nk, 64, any));
+    FV_TRY(make_head_map(&m3, *v, g, g.Hk, g.Nk, 64, any));
+    a.tiles = q_tiles;
+    a.n_items = g.B * g.H * q_tiles;
+    a.heavy_tiles = 0;
+    a.out0 = WinOut{dq->data, dq->batch, dq->head, dq->token};
+    StageTimer t(FVATTN_STAGE_WINDOW_Q, s);
+    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, false, dev.sms, s));
+    t.kernels = 1;
+  }
   return FVATTN_OK;
 }
 

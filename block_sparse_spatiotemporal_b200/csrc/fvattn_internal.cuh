@@ -217,6 +217,24 @@ struct WinFwdArgs {
   long long wait_cap;
 };
 
+struct WinOut {                    // a [B, heads, tokens, D] tensor, strides in elements
+  void* data;
+  long long batch, head, token;
+};
+// Backward of the sliding-window attention (both kernels of the template).
+struct WinBwdArgs {
+  WinGeom g;
+  int tiles;                       // 128-row stationary tiles of a (batch, head)
+  int heavy_tiles;                 // key-stationary: tiles that hold sinks, run first
+  int n_items;
+  const float* lse2;               // [B, H, Nq] lse * log2(e)
+  const float* dd;                 // [B, H, Nq] rowsum(dout * out)
+  WinOut out0;                     // dK (key-stationary) or dQ
+  WinOut out1;                     // dV (key-stationary)
+  int* status;
+  long long wait_cap;
+};
+
 struct FineF32Args {
   Geom g;
   const float* q;
@@ -609,6 +627,11 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const void* x, const v
                             int num_sms, cudaStream_t s);
 cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
                               int num_sms, cudaStream_t s);
+cudaError_t launch_window_prep(const WinGeom& g, const WinOut& out, const WinOut& dout, const float* lse, float* lse2,
+                               float* dd, cudaStream_t s);
+cudaError_t launch_window_bwd(const CUtensorMap& s0, const CUtensorMap& s1, const CUtensorMap& m0,
+                              const CUtensorMap& m1, const WinBwdArgs& a, bool key_stationary, int num_sms,
+                              cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, long long cap, cudaStream_t s);
 
 }  // namespace fvattn

@@ -26,7 +26,7 @@ __all__ = [
     "STAGES", "pool_select_noalloc", "noalloc_status", "profile_cta_times", "workspace_size_qkv", "qkv_rope", "workspace_size_bwd", "block_sparse_bwd",
     "augment_lists", "block_sparse_fwd_worklist", "timestep_params",
     "Norm", "Window", "View", "make_norm", "norm_workspace", "layer_norm_fwd", "layer_norm_bwd",
-    "make_window", "window_workspace", "window_fwd",
+    "make_window", "window_workspace", "window_fwd", "window_bwd",
 ]
 
 F32, BF16 = 0, 1
@@ -149,6 +149,9 @@ _SIGS = {
     "fvattn_window_fwd": [ctypes.POINTER(Window), ctypes.POINTER(View), ctypes.POINTER(View), ctypes.POINTER(View),
                           ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(View), ctypes.c_void_p, ctypes.c_void_p,
                           ctypes.c_size_t, ctypes.c_void_p],
+    "fvattn_workspace_size_window_bwd": [ctypes.POINTER(Window), ctypes.POINTER(ctypes.c_size_t)],
+    "fvattn_window_bwd": [ctypes.POINTER(Window)] + [ctypes.POINTER(View)] * 5 + [ctypes.c_void_p] * 3 +
+                         [ctypes.POINTER(View)] * 3 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p],
     "fvattn_get_device_status": [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)],
     "fvattn_selftest_wait_timeout": [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_void_p],
     "fvattn_profile_enable": [ctypes.c_int],
@@ -157,7 +160,7 @@ _SIGS = {
 }
 
 STAGES = ("tables", "reorder", "pool", "select", "schedule", "fine", "prologue", "bwd_prep", "bwd_kv", "bwd_q",
-          "norm", "norm_bwd", "window")
+          "norm", "norm_bwd", "window", "window_prep", "window_kv", "window_q")
 
 
 def lib():
@@ -584,10 +587,16 @@ def make_window(batch, heads, head_dim, q_len, kv_len, window, sinks=0, unit=1, 
 
 
 def window_workspace(win: Window, backward=False, device="cuda") -> torch.Tensor:
-    """A device workspace for window_fwd (caller-owned)."""
+    """A device workspace for window_fwd, or (backward) one that serves
+    window_fwd and window_bwd in turn (caller-owned)."""
     n = ctypes.c_size_t()
     _check("fvattn_workspace_size_window", lib().fvattn_workspace_size_window(ctypes.byref(win), ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+    size = n.value
+    if backward:
+        _check("fvattn_workspace_size_window_bwd",
+               lib().fvattn_workspace_size_window_bwd(ctypes.byref(win), ctypes.byref(n)))
+        size = max(size, n.value)
+    return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _view(t: torch.Tensor, batch: int, heads: int, tokens: int, d: int, what: str):
@@ -627,6 +636,27 @@ def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, ls
                                        _view(out, B, H, win.q_len, D, "out"),
                                        _typed(lse, torch.float32, (B, H, win.q_len), "lse"), _ptr(ws), ws.numel(), s))
     return out, lse
+
+
+def window_bwd(win: Window, q, k, v, out, dout, lse, ws, q_lens=None, kv_lens=None, grads=None, stream=None):
+    """Backward of window_fwd (ws from ``window_workspace(win, backward=True)``):
+    returns (dq, dk, dv).  grads: the three output tensors."""
+    B, H, Hk, D = win.batch, win.heads, win.kv_heads, win.head_dim
+    with _Launch((q, k, v, out, dout, lse, ws, q_lens, kv_lens, *(grads or ())), stream) as s:
+        vq, vk, vv = (_view(q, B, H, win.q_len, D, "q"), _view(k, B, Hk, win.kv_len, D, "k"),
+                      _view(v, B, Hk, win.kv_len, D, "v"))
+        if grads is None:
+            grads = (_new_heads(q, q_lens), _new_heads(k, kv_lens), _new_heads(v, kv_lens))
+        dq, dk, dv = grads
+        _check("fvattn_window_bwd",
+               lib().fvattn_window_bwd(ctypes.byref(win), vq, vk, vv, _view(out, B, H, win.q_len, D, "out"),
+                                       _view(dout, B, H, win.q_len, D, "dout"),
+                                       _typed(lse, torch.float32, (B, H, win.q_len), "lse"),
+                                       _typed(q_lens, torch.int32, (B,), "q_lens"),
+                                       _typed(kv_lens, torch.int32, (B,), "kv_lens"),
+                                       _view(dq, B, H, win.q_len, D, "dq"), _view(dk, B, Hk, win.kv_len, D, "dk"),
+                                       _view(dv, B, Hk, win.kv_len, D, "dv"), _ptr(ws), ws.numel(), s))
+    return dq, dk, dv
 
 
 def device_status(ws, stream=None) -> int:

@@ -415,6 +415,24 @@ int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvat
                       const int32_t* q_lens, const int32_t* kv_lens, const fvattn_view* out, float* lse, void* ws,
                       size_t ws_bytes, fvattn_stream_t stream);
 
+/* Backward of fvattn_window_fwd: for its out and lse and the gradient dout of
+ * out, with p = exp(scale q k^T - lse) over the visible pairs,
+ *   dv = p^T dout,  ds = p * (dout v^T - rowsum(dout * out)),
+ *   dq = scale ds k,  dk = scale ds^T q,
+ * dk and dv summed over the query heads that share a KV head; a key no query
+ * sees gets zero gradients, a query that sees no key dq = 0.  Shapes, strides,
+ * lengths and the contents of unseen rows as in fvattn_window_fwd (out and
+ * dout like q; rows of dq behind q_lens and of dk, dv behind kv_lens are not
+ * written; rows of q, out and dout behind q_lens may hold anything).  P and
+ * dS are rounded to bf16 for the tensor cores, accumulation is fp32, the
+ * gradients are rounded once to bf16.  No atomics: deterministic.
+ * Workspace: fvattn_workspace_size_window_bwd bytes. */
+int fvattn_workspace_size_window_bwd(const fvattn_window* win, size_t* bytes);
+int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvattn_view* k, const fvattn_view* v,
+                      const fvattn_view* out, const fvattn_view* dout, const float* lse, const int32_t* q_lens,
+                      const int32_t* kv_lens, const fvattn_view* dq, const fvattn_view* dk, const fvattn_view* dv,
+                      void* ws, size_t ws_bytes, fvattn_stream_t stream);
+
 /* Synchronises the stream, reads and clears the workspace status word.
  * *status is 0 or a positive code: 1 bad block id, 2 wait cap reached. */
 int fvattn_get_device_status(void* ws, fvattn_stream_t stream, int32_t* status);
@@ -447,7 +465,10 @@ typedef enum {
   FVATTN_STAGE_NORM = 10,     /* layer norm, forward */
   FVATTN_STAGE_NORM_BWD = 11, /* layer norm, backward */
   FVATTN_STAGE_WINDOW = 12,   /* sliding-window attention, forward */
-  FVATTN_STAGE_COUNT = 13
+  FVATTN_STAGE_WINDOW_PREP = 13, /* its backward: rowsum(dout * out), lse * log2(e) */
+  FVATTN_STAGE_WINDOW_KV = 14,   /* its backward: key-stationary dK, dV kernel */
+  FVATTN_STAGE_WINDOW_Q = 15,    /* its backward: query-stationary dQ kernel */
+  FVATTN_STAGE_COUNT = 16
 } fvattn_stage;
 int fvattn_profile_enable(int enable);
 int fvattn_profile_read(double* ms, int64_t* launches);

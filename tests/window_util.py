@@ -41,7 +41,7 @@ def plain_fwd(q, k, v, unit, window, sinks, scale=None, q_lens=None, kv_lens=Non
 
 def plain_bwd(q, k, v, dout, unit, window, sinks, scale=None, q_lens=None, kv_lens=None):
     """(dq, dk, dv) in float64 and the error scales (a |k|, a^T |q|, p^T |dout|)
-    with a = scale p (|dp| + sum |dout out|); rows behind the lengths are 0."""
+    with a = scale p (|dp| + sum |dout| p|v|); rows behind the lengths are 0."""
     B, H, Nq, D = q.shape
     Hk, Nk = k.shape[1], k.shape[2]
     G = H // Hk
@@ -64,7 +64,7 @@ def plain_bwd(q, k, v, dout, unit, window, sinks, scale=None, q_lens=None, kv_le
         o = p @ vs
         dp = do @ vs.transpose(1, 2)
         ds = p * (dp - (do * o).sum(-1, keepdim=True))
-        a = scale * p * (dp.abs() + (do * o).abs().sum(-1, keepdim=True))
+        a = scale * p * (dp.abs() + (do.abs() * (p @ vs.abs())).sum(-1, keepdim=True))
         heads = lambda t: t.reshape(Hk, G, kl, D).sum(1)  # noqa: E731
         g[0][b, :, :ql], e[0][b, :, :ql] = scale * ds @ ks, a @ ks.abs()
         g[1][b, :, :kl], e[1][b, :, :kl] = heads(scale * ds.transpose(1, 2) @ qs), heads(a.transpose(1, 2) @ qs.abs())
