@@ -723,8 +723,11 @@ constexpr int kWinSms = 148;
 
 // Tiling of the forward: heads packed into a tile when a tile of one head's
 // queries would stay partly empty, items of two query tiles unless one holds
-// all queries, and the key tiles split when there are fewer items than SMs
-// (each split at least four key tiles).
+// all queries, and the key tiles of an item split where that shortens the
+// longest CTA's work: rounds of items over the SMs times (steps of an item +
+// what an item costs besides, in steps: 4 for an item of two query tiles, 6
+// when its parts have to be joined, 1 for few queries, whose loads run ahead
+// over item borders and whose parts are small).
 int win_plan(const WinGeom& g, WinFwdArgs* a) {
   a->g = g;
   a->pack = g.Nq < 128 && g.G <= 128 ? g.G : 1;
@@ -733,18 +736,24 @@ int win_plan(const WinGeom& g, WinFwdArgs* a) {
   a->dual = tiles > 1;
   a->item_tiles = a->dual ? (tiles + 1) / 2 : tiles;
   const int64_t items = (int64_t)g.B * g.Hk * (g.G / a->pack) * a->item_tiles;
-  if (items > (1 << 28)) return FVATTN_ERR_SHAPE;
+  if (items > (1 << 26)) return FVATTN_ERR_SHAPE;
+  int64_t keys = g.Nk;
+  if (g.window > 0) {
+    const int64_t w = ((int64_t)g.window + (g.unit > 1 ? 1 : 0)) * g.unit + (int64_t)a->tokens * (a->dual ? 2 : 1) +
+                      (int64_t)g.sinks * g.unit;
+    keys = w < keys ? w : keys;
+  }
+  const int64_t steps = (keys + 127) / 128;
   a->splits = 1;
-  if (items > 0 && items < kWinSms) {
-    int64_t keys = g.Nk;
-    if (g.window > 0) {
-      const int64_t w = ((int64_t)g.window + 1) * g.unit + (int64_t)a->tokens * (a->dual ? 2 : 1) +
-                        (int64_t)g.sinks * g.unit;
-      keys = w < keys ? w : keys;
+  if (items > 0 && items < 8 * kWinSms) {
+    int64_t best = 0;
+    for (int64_t s = 1; s <= 64 && (s == 1 || s <= (a->dual ? steps / 4 : (steps + 1) / 2)); ++s) {
+      const int64_t cost = ((items * s + kWinSms - 1) / kWinSms) * ((steps + s - 1) / s + (a->dual ? (s > 1 ? 6 : 4) : 1));
+      if (s == 1 || cost < best) {
+        best = cost;
+        a->splits = (int)s;
+      }
     }
-    const int64_t most = ((keys + 127) / 128) / 4;
-    const int64_t want = kWinSms / items;
-    a->splits = (int)(most < 1 ? 1 : want < most ? want : most);
   }
   a->parts = a->dual ? a->splits : 2 * a->splits;
   a->n_items = (int)(items * a->splits);
@@ -752,12 +761,13 @@ int win_plan(const WinGeom& g, WinFwdArgs* a) {
 }
 
 struct WinWs {
-  size_t counters, part_lse, part_o, total, zeroed;
+  size_t next_item, counters, part_lse, part_o, total, zeroed;
 };
 WinWs win_ws(const WinFwdArgs& a) {
   WinWs L{};
-  size_t off = kAlign;               // status word
-  L.zeroed = sizeof(int);
+  size_t off = kAlign;               // status word, item counter
+  L.next_item = sizeof(int);
+  L.zeroed = 2 * sizeof(int);
   if (a.parts > 1) {
     const size_t rows = (size_t)a.n_items * 2 * a.tokens * a.pack;
     L.counters = off;
@@ -1277,6 +1287,7 @@ int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvat
     a.part_o = reinterpret_cast<float*>(base + L.part_o);
     a.counters = reinterpret_cast<int*>(base + L.counters);
   }
+  a.next_item = reinterpret_cast<int*>(base + L.next_item);
   a.status = reinterpret_cast<int*>(base);
   a.wait_cap = kDefaultWaitCap;
   StageTimer t(FVATTN_STAGE_WINDOW, s);

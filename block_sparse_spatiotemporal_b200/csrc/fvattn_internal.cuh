@@ -212,7 +212,8 @@ struct WinFwdArgs {
   float* lse;                      // [B, H, Nq]
   float* part_o;                   // [n_items][2][tokens * pack][D]
   float* part_lse;                 // [n_items][2][tokens * pack], base 2
-  int* counters;
+  int* counters;                   // parts written, per item and query tile
+  int* next_item;                  // zeroed: items handed out after each CTA's first
   int* status;
   long long wait_cap;
 };

@@ -42,6 +42,10 @@ __device__ inline Span span_of(const WinGeom& g, const Seq& s, int i) {
   return {u0 * g.unit, hi, sk < hi ? (int)sk : hi};
 }
 
+// The value of lane 0, which the compiler then knows to be the same in every
+// lane: operands of the matrix instructions stay in uniform registers.
+__device__ inline uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Bits a .. b - 1 of a 32-bit word (a and b may lie outside it).
 __device__ inline uint32_t bits(int a, int b) {
   a = a < 0 ? 0 : a;
@@ -57,6 +61,15 @@ __device__ inline void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ inline void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 __device__ inline void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {

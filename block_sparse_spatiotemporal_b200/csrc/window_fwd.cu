@@ -12,29 +12,37 @@
 //
 // Persistent kernel, one CTA per SM, 384 threads, over items of two 128-row
 // query tiles A, B that share one stream of 128-key tiles:
-//   warp 0       TMA: the item's Q, then K and V tiles through one ring;
-//   warp 1       MMAs: per step j and tile g, O_g += P_g(j-1) V, then
+//   warp 0       TMA: takes the CTA's next item from a counter, publishes it
+//                in a ring in shared memory (the other warps would each spend
+//                3,000 clocks on its divisions), loads its Q and its K and V
+//                tiles, these through one ring;
+//   warps 1, 2   MMAs of tile A, B: per step O_g += P_g(j-1) V in two halves
+//                of 64 keys as the softmax hands them over, then
 //                S_g(j) = Q_g K^T into the TMEM columns P_g(j-1) held (MMAs
-//                of one thread run in issue order), so while one tile's
-//                softmax runs the other tile's products keep the tensor
-//                cores fed;
+//                of one thread run in issue order).  While one tile's softmax
+//                runs, the other's products keep the tensor cores fed;
 //   warps 4-7, 8-11   softmax of tile A, B: thread r owns row r; P is
 //                written back over S as bf16 (the A operand of the PV MMA;
 //                its rounding, relative 2^-9, is the step's largest error).
 // Key tiles that none of a tile's rows sees are skipped for that tile, and
-// only tiles that some row sees in part are masked.
+// only tiles that some row sees in part are masked.  Output rows go through
+// shared memory so that a store writes whole 128-byte lines (a thread storing
+// its own row took 6,400 clocks an item).
 //
 // Few queries (at most 128 rows a KV head, the query heads of a KV head
 // packed into one tile when there are fewer than 128 queries): both softmax
 // groups work on the same query tile, on alternate key tiles, and the key
-// tiles of an item are split over several CTAs.  Each group writes its
-// normalised part and its lse to the workspace, and the last one to arrive
-// (a counter per item) joins the parts in ascending order, so the result
-// does not depend on which that is.
+// tiles of an item are split over several CTAs.  Bound by the reading of K
+// and V, this form has tensor time to spare and gives P a second bf16 for
+// what the first one rounds away (a second PV product).  Each group writes
+// its normalised part and its lse to the workspace, and the last one to
+// arrive (a counter per item) joins the parts in ascending order, so the
+// result does not depend on which that is.
 //
-// TMEM (512 columns): S_A, S_B at 0, 128 (P over the first 64 of each), O_A,
-// O_B at 256, 384.  Shared memory: Q 2 x 128 rows, ring of 128-key tiles, all
-// in 128-byte swizzled parts of 64 dims.
+// TMEM (512 columns): S_A, S_B at 0, 128 (each half's P over its first 32
+// columns, its second bf16 over the others), O_A, O_B at 256, 384.  Shared memory: Q 2 x
+// 128 rows, ring of 128-key tiles, all in 128-byte swizzled parts of 64 dims;
+// 4 KB a softmax warp for the output.
 #include "window.cuh"
 
 namespace fvattn {
@@ -46,27 +54,47 @@ constexpr uint32_t PART = 128 * 128;         // 64 dims of 128 rows: 16 KB
 constexpr float RESCALE_SUM = 18446744073709551616.f;   // 2^64
 constexpr uint32_t TMEM_COLS = 512, TM_S = 0, TM_O = 256;
 
+constexpr int ITEMS = 2;                     // items published ahead
+constexpr uint32_t OUT_STAGE = 32 * 128;     // 32 rows x 128 bytes a softmax warp
+
 template <int D> struct Cfg {
   static constexpr int PARTS = D / 64;
   static constexpr uint32_t TILE = PART * PARTS;        // 128 rows
-  static constexpr int NST = D == 128 ? 5 : 10;         // ring of K and V tiles
-  static constexpr uint32_t SMEM = 1024 + 2 * TILE + NST * TILE;
+  static constexpr int NST = D == 128 ? 4 : 8;          // ring of K and V tiles
+  static constexpr uint32_t SMEM = 1024 + 2 * TILE + NST * TILE + 8 * OUT_STAGE;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
 };
 
+// Item and its key tiles.
+struct Item {
+  int idx;               // -1: the CTA has no further item
+  int b, hk, g0;         // batch, KV head, first query head of the tile within the KV head's (0 when packed)
+  int tile;              // first 128-row query tile
+  int split;
+  Seq seq;
+  int ns, t_lo, n;       // steps 0 .. ns - 1 are key tiles 0 .., the others t_lo, t_lo + 1, ..; n steps in all
+  int j0, j1;            // this split's steps
+  int a_lo[2], a_hi[2], a_sk[2];   // query tile g works on key tiles [a_lo, a_hi) and, below, [0, a_sk)
+  int dead_lo, dead_sk;  // keys in [dead_sk, dead_lo) are seen by no query of the sequence
+  __device__ int key_tile(int j) const { return j < ns ? j : t_lo + j - ns; }
+};
+
 struct FwdCtl {
+  uint64_t item_full[ITEMS], item_empty[ITEMS];   // 2 MMA warps and 8 softmax warps read an item
   uint64_t q_full, q_empty;
-  uint64_t kv_full[10], kv_empty[10];
-  uint64_t s_full[2];    // S_g of its next step written (and every earlier MMA complete)
-  uint64_t p_full[2];    // P_g written (4 warps)
-  uint64_t o_full[2];    // the item's last PV of tile g complete
-  uint64_t o_empty[2];   // O_g read (4 warps)
-  uint64_t group[2];     // softmax group t meets (4 warps), twice per item with parts
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2];      // S_g of its next step written (and every earlier MMA of the tile complete)
+  uint64_t p_full[2][2];   // half h of P_g written (4 warps)
+  uint64_t pv_half[2];     // PV of the first half of P_g complete
+  uint64_t o_full[2];      // the item's last PV of tile g complete
+  uint64_t o_empty[2];     // O_g read (4 warps)
+  uint64_t group[2];       // softmax group t meets (4 warps)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int last[2];           // this group's part was the item's last
+  int last[2];             // this group's part was the item's last
+  Item item[ITEMS];
 };
 static_assert(Cfg<128>::SMEM + sizeof(FwdCtl) <= 232448 && Cfg<64>::SMEM + sizeof(FwdCtl) <= 232448, "shared memory");
 
@@ -99,10 +127,11 @@ __device__ inline void exp2_poly2(uint64_t X, float& y0, float& y1) {
   y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(q1) << 23));
 }
 
-// P of 32 logits as 16 bf16x2 words, their fp32 sum added to acc.
-template <bool MASKED>
+// P of 32 logits as 16 bf16x2 words (and what they round away as 16 more),
+// their fp32 sum added to acc.
+template <bool MASKED, bool TWO>
 __device__ inline void exp_chunk(const uint32_t (&s)[32], uint64_t SL, uint64_t NM, uint32_t mask, uint32_t* pk,
-                                 uint64_t (&acc)[2]) {
+                                 uint32_t* lo, uint64_t (&acc)[2]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float a = __uint_as_float(s[2 * i]), b = __uint_as_float(s[2 * i + 1]);
@@ -112,7 +141,7 @@ __device__ inline void exp_chunk(const uint32_t (&s)[32], uint64_t SL, uint64_t 
     }
     const uint64_t X = fma2(f2(a, b), SL, NM);
     float p0, p1;
-    if (!MASKED && poly_pair(i)) {
+    if (!MASKED && !TWO && poly_pair(i)) {
       exp2_poly2(X, p0, p1);
     } else {
       float x0, x1;
@@ -121,7 +150,9 @@ __device__ inline void exp_chunk(const uint32_t (&s)[32], uint64_t SL, uint64_t 
       p1 = ex2(x1);
     }
     acc[i & 1] = add2(acc[i & 1], f2(p0, p1));
-    pk[i] = cvt_bf16x2(p0, p1);
+    const uint32_t w = cvt_bf16x2(p0, p1);
+    pk[i] = w;
+    if (TWO) lo[i] = cvt_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xFFFF0000u));
   }
 }
 
@@ -129,62 +160,39 @@ __device__ inline uint32_t chunk_mask(const Span& sp, int key0) {
   return bits(sp.lo - key0, sp.hi - key0) | bits(0, sp.sk - key0);
 }
 
-// Row of 128 logits at tS: P (64 words) and the sum of its values.
-template <bool MASKED>
-__device__ inline float exp_row(uint32_t tS, float sl2, float m, const Span& sp, int key0, uint32_t (&pk)[64]) {
+// P of a row's 64 logits and their sum.
+template <bool MASKED, bool TWO>
+__device__ inline float exp_half(const uint32_t (&s0)[32], const uint32_t (&s1)[32], float sl2, float m, const Span& sp,
+                                 int key0, uint32_t (&pk)[32], uint32_t (&lo)[TWO ? 32 : 1]) {
   const uint64_t SL = f2(sl2, sl2), NM = f2(-m, -m);
   uint64_t acc[2] = {0ull, 0ull};
-#pragma unroll
-  for (int c = 0; c < 4; c += 2) {
-    uint32_t s0[32], s1[32];
-    tmem_ld32(tS + 32 * c, s0);
-    tmem_ld32(tS + 32 * c + 32, s1);
-    tmem_wait_ld();
-    exp_chunk<MASKED>(s0, SL, NM, MASKED ? chunk_mask(sp, key0 + 32 * c) : 0u, pk + 16 * c, acc);
-    exp_chunk<MASKED>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32 * c + 32) : 0u, pk + 16 * c + 16, acc);
-  }
-  float a, b;
-  uf2(add2(acc[0], acc[1]), a, b);
-  return a + b;
+  exp_chunk<MASKED, TWO>(s0, SL, NM, MASKED ? chunk_mask(sp, key0) : 0u, pk, lo, acc);
+  exp_chunk<MASKED, TWO>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32) : 0u, pk + 16, TWO ? lo + 16 : lo, acc);
+  return sum2(add2(acc[0], acc[1]));
 }
 
-// Largest visible logit of the row (-inf: none).
-__device__ inline float row_max(uint32_t tS, const Span& sp, int key0) {
+// Largest visible of a row's 64 logits (-inf: none).
+__device__ inline float max_half(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const Span& sp, int key0) {
+  const uint32_t m0 = chunk_mask(sp, key0), m1 = chunk_mask(sp, key0 + 32);
   float m = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t s[32];
-    tmem_ld32(tS + 32 * c, s);
-    tmem_wait_ld();
-    const uint32_t mask = chunk_mask(sp, key0 + 32 * c);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if ((mask >> i) & 1u) m = fmaxf(m, __uint_as_float(s[i]));
+  for (int i = 0; i < 32; ++i) {
+    if ((m0 >> i) & 1u) m = fmaxf(m, __uint_as_float(s0[i]));
+    if ((m1 >> i) & 1u) m = fmaxf(m, __uint_as_float(s1[i]));
   }
   return m;
 }
 
-// Item and its key tiles, the same for every warp.
-struct Item {
-  int b, hk, g0;         // batch, KV head, first query head of the tile within the KV head's (0 when packed)
-  int tile;              // first 128-row query tile
-  int split;
-  Seq seq;
-  int ns, t_lo, n;       // steps 0 .. ns - 1 are tiles 0 .., the others t_lo, t_lo + 1, ..; n steps in all
-  int j0, j1;            // this split's steps
-  int lo[2], hi[2], sk[2];   // of query tile g: smallest lo, largest hi and sk of its rows
-  int dead_lo, dead_sk;  // keys in [dead_sk, dead_lo) are seen by no query of the sequence
-  __device__ int key0(int j) const { return 128 * (j < ns ? j : t_lo + j - ns); }
-};
-
-__device__ inline Item item_of(const WinFwdArgs& a, int idx) {
+__device__ inline Item item_of(const WinFwdArgs& a, int idx0) {
   const WinGeom& g = a.g;
   Item it;
+  it.idx = idx0;
+  unsigned idx = idx0;
   it.split = idx % a.splits;
   idx /= a.splits;
   const int qt = idx % a.item_tiles;
   idx /= a.item_tiles;
-  const int per_kv = g.G / a.pack;             // head slots of a KV head
+  const unsigned per_kv = g.G / a.pack;        // head slots of a KV head
   it.g0 = idx % per_kv;
   idx /= per_kv;
   it.hk = idx % g.Hk;
@@ -194,23 +202,23 @@ __device__ inline Item item_of(const WinFwdArgs& a, int idx) {
   int lo = 0x7fffffff, hi = 0, sk = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    it.lo[t] = it.hi[t] = it.sk[t] = 0;
+    it.a_lo[t] = it.a_hi[t] = it.a_sk[t] = 0;
     const int i0 = (it.tile + (a.dual ? t : 0)) * a.tokens;
     if (i0 >= it.seq.ql) continue;
     const int i1 = i0 + a.tokens < it.seq.ql ? i0 + a.tokens : it.seq.ql;
     const Span last = span_of(g, it.seq, i1 - 1);
     if (last.hi == 0) continue;
     const int first_pos = it.seq.ql - it.seq.kvl;          // first query that is not in front of the keys
-    it.lo[t] = span_of(g, it.seq, i0 > first_pos ? i0 : first_pos).lo;
-    it.hi[t] = last.hi;
-    it.sk[t] = last.sk;
-    lo = it.lo[t] < lo ? it.lo[t] : lo;
-    hi = it.hi[t] > hi ? it.hi[t] : hi;
-    sk = it.sk[t] > sk ? it.sk[t] : sk;
+    const int lo_t = span_of(g, it.seq, i0 > first_pos ? i0 : first_pos).lo;
+    it.a_lo[t] = lo_t >> 7;
+    it.a_hi[t] = (last.hi + 127) >> 7;
+    it.a_sk[t] = (last.sk + 127) >> 7;
+    lo = lo_t < lo ? lo_t : lo;
+    hi = last.hi > hi ? last.hi : hi;
+    sk = last.sk > sk ? last.sk : sk;
   }
-  if (hi == 0) {
-    it.ns = it.t_lo = it.n = 0;
-  } else {
+  it.ns = it.t_lo = it.n = 0;
+  if (hi > 0) {
     const int t_hi = (hi + 127) >> 7, ns = (sk + 127) >> 7;
     it.t_lo = lo >> 7;
     it.ns = ns < it.t_lo ? ns : 0;
@@ -227,14 +235,37 @@ __device__ inline Item item_of(const WinFwdArgs& a, int idx) {
   return it;
 }
 
-// Does softmax group / accumulator t work on step j?
-__device__ inline bool active(const WinFwdArgs& a, const Item& it, int t, int j) {
-  const int k0 = it.key0(j);
-  if (!a.dual && ((j - it.j0) & 1) != t) return false;
-  return k0 < it.hi[t] && (k0 + 128 > it.lo[t] || k0 < it.sk[t]);
+// The key tiles of one query tile (dual) or one group's turns (single).
+template <bool DUAL> struct Turn {
+  int lo, hi, sk, j0, t;
+  __device__ Turn(const Item& it, int t_) : lo(it.a_lo[t_]), hi(it.a_hi[t_]), sk(it.a_sk[t_]), j0(it.j0), t(t_) {}
+  __device__ bool on(int j, int key_tile) const {
+    return DUAL ? key_tile < hi && (key_tile >= lo || key_tile < sk) : ((j - j0) & 1) == t;
+  }
+};
+
+// Writes 128 bytes of each of the warp's 32 rows (lane r: row r, 32 words in
+// v) to the rows' own addresses through the warp's staging: eight lanes write
+// a row's line.  Chunks of 16 bytes are swizzled by the row against bank
+// conflicts.
+__device__ inline void store_rows(uint8_t* stage, const uint32_t (&v)[32], uint8_t* row_ptr, bool valid) {
+  const int lane = threadIdx.x & 31;
+  uint4* st = reinterpret_cast<uint4*>(stage);
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st[lane * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  const unsigned mask = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 3), c = lane & 7;
+    const unsigned long long p = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_ptr), row);
+    if ((mask >> row) & 1u) reinterpret_cast<uint4*>(p)[c] = st[row * 8 + (c ^ (row & 7))];
+  }
+  __syncwarp();
 }
 
-template <int D>
+template <int D, bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mv, const WinFwdArgs a) {
@@ -243,6 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * C::TILE;
+  uint8_t* sOut = sKV + C::NST * C::TILE;
   __shared__ FwdCtl ctl_s;
   FwdCtl* ctl = &ctl_s;
   volatile int* abort_flag = &ctl->abort;
@@ -251,20 +283,26 @@ __global__ void __launch_bounds__(THREADS, 1)
   const long long cap = a.wait_cap;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&ctl->item_full[i], 1);
+      mbar_init(&ctl->item_empty[i], 10);
+    }
     mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 1);
+    mbar_init(&ctl->q_empty, 2);
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
-      mbar_init(&ctl->kv_empty[i], 1);
+      mbar_init(&ctl->kv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->p_full[i][0], 4);
+      mbar_init(&ctl->p_full[i][1], 4);
+      mbar_init(&ctl->pv_half[i], 1);
       mbar_init(&ctl->o_full[i], 1);
       mbar_init(&ctl->o_empty[i], 4);
       mbar_init(&ctl->group[i], 4);
     }
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain, 2);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -284,14 +322,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       prefetch_tensormap(&mk);
       prefetch_tensormap(&mv);
       long long seq = 0;
-      int k = 0, q_issued = 0;
+      int q_issued = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
+      int idx = blockIdx.x;
+      for (int n = 0;; ++n) {
+        const int ib = n % ITEMS;
+        if (n >= ITEMS && !mbar_wait(&ctl->item_empty[ib], (uint32_t)(n / ITEMS - 1) & 1, abort_flag, a.status, cap))
+          break;
+        if (idx >= a.n_items) {
+          ctl->item[ib].idx = -1;
+          mbar_arrive(&ctl->item_full[ib]);
+          break;
+        }
         const Item it = item_of(a, idx);
+        ctl->item[ib] = it;
+        mbar_arrive(&ctl->item_full[ib]);
+        idx = gridDim.x + atomicAdd(a.next_item, 1);        // the one after this
         if (it.j0 >= it.j1) continue;
-        if (k >= 1 && !mbar_wait(&ctl->q_empty, (uint32_t)(k - 1) & 1, abort_flag, a.status, cap)) break;
-        ++k;
-        const int tiles = a.dual ? 2 : 1;
+        if (q_issued >= 1 && !mbar_wait(&ctl->q_empty, (uint32_t)(q_issued - 1) & 1, abort_flag, a.status, cap)) break;
+        const int tiles = DUAL ? 2 : 1;
         mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(tiles * C::PARTS * a.pack * a.tokens) * 128u);
         for (int t = 0; t < tiles; ++t)
           for (int h = 0; h < C::PARTS; ++h)
@@ -299,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         it.b);
         ++q_issued;
         for (int j = it.j0; j < it.j1 && ok; ++j) {
-          const int key0 = it.key0(j);
+          const int key0 = 128 * it.key_tile(j);
           for (int kv = 0; kv < 2; ++kv, ++seq) {
             const int st = (int)(seq % C::NST);
             if (seq >= C::NST &&
@@ -312,6 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               tma_load_4d(sKV + st * C::TILE + h * PART, kv ? &mv : &mk, &ctl->kv_full[st], 64 * h, key0, it.hk, it.b);
           }
         }
+        if (!ok) break;
       }
       // every copy issued has landed before the block exits
       if (q_issued >= 1) mbar_drain(&ctl->q_full, (uint32_t)(q_issued - 1) & 1, a.status, cap);
@@ -320,94 +370,109 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(&ctl->kv_full[i], (uint32_t)(last / C::NST) & 1, a.status, cap);
       }
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------- MMAs of tile t
+    const int t = warp - 1;
     long long seq = 0;               // ring number of the K tile of the item's first step
-    int k = 0;
-    long long cnt[2] = {0, 0};       // steps done of each tile
-    int items[2] = {0, 0};           // items whose O_g was written
+    int q_items = 0;                 // items with steps
+    uint32_t cnt = 0;                // steps of this tile
+    int items = 0;                   // items whose O_t was written
     bool ok = true;
-    const uint32_t q_base = smem_u32(sQ), kv_base = smem_u32(sKV);
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item it = item_of(a, idx);
-      if (it.j0 >= it.j1) continue;
-      if (!mbar_wait_warp(&ctl->q_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
-      ++k;
-      bool first[2] = {true, true};
-      for (int j = it.j0; j <= it.j1 && ok; ++j) {
-        const long long sk = seq + 2ll * (j - it.j0), sv = sk - 1;     // K of step j, V of step j - 1
+    const uint32_t qt = uni(smem_u32(sQ) + (DUAL ? t : 0) * C::TILE), kv_base = smem_u32(sKV);
+    const uint32_t tS = uni(tbase + TM_S + 128 * t), tO = uni(tbase + TM_O + 128 * t);
+    for (int n = 0; ok; ++n) {
+      const int ib = n % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item& si = ctl->item[ib];
+      const int idx = si.idx, j0 = si.j0, j1 = si.j1, ns = si.ns, t_lo = si.t_lo, kvl = si.seq.kvl;
+      const int dead_lo = si.dead_lo, dead_sk = si.dead_sk;
+      const Turn<DUAL> turn(si, t);
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      if (idx < 0) break;
+      if (j0 >= j1) continue;
+      if (!mbar_wait_warp(&ctl->q_full, (uint32_t)q_items & 1, abort_flag, a.status, cap)) break;
+      ++q_items;
+      bool first = true, prev = false;
+      int prev_key0 = 0;
+      for (int j = j0; j <= j1; ++j) {
+        const long long sk = seq + 2ll * (j - j0), sv = sk - 1;     // K of step j, V of step j - 1
         const int stk = (int)(sk % C::NST), stv = (int)(sv % C::NST);
-        if (j < it.j1 && !mbar_wait_warp(&ctl->kv_full[stk], (uint32_t)(sk / C::NST) & 1, abort_flag, a.status, cap)) {
-          ok = false;
-          break;
-        }
-        if (j > it.j0) {
+        const uint32_t k_at = uni(kv_base + stk * C::TILE), v_at = uni(kv_base + stv * C::TILE);
+        const int kt = j < ns ? j : t_lo + j - ns;
+        const bool now = j < j1 && turn.on(j, kt);
+        if (j > j0) {
           if (!mbar_wait_warp(&ctl->kv_full[stv], (uint32_t)(sv / C::NST) & 1, abort_flag, a.status, cap)) {
             ok = false;
             break;
           }
-          // values that no query of the sequence sees may be anything: their
-          // probabilities are 0, and 0 times NaN is not
-          const int key0 = it.key0(j - 1);
-          if (key0 + 128 > it.seq.kvl && it.seq.kvl < g.Nk)
-            zero_rows(sKV + stv * C::TILE, PART, C::PARTS, it.seq.kvl - key0, 128);
-          if (key0 < it.dead_lo && key0 + 128 > it.dead_sk)
-            zero_rows(sKV + stv * C::TILE, PART, C::PARTS, it.dead_sk > key0 ? it.dead_sk - key0 : 0,
-                      it.dead_lo - key0 < 128 ? it.dead_lo - key0 : 128);
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j > it.j0 && active(a, it, t, j - 1)) {
-            if (first[t] && items[t] >= 1 &&
-                !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items[t] - 1) & 1, abort_flag, a.status, cap)) {
+          if (prev) {
+            // values that no query of the sequence sees may be anything: their
+            // probabilities are 0, and 0 times NaN is not.  (Both tiles' warps
+            // write the same zeros before they use the tile.)
+            if (prev_key0 + 128 > kvl && kvl < g.Nk)
+              zero_rows(sKV + stv * C::TILE, PART, C::PARTS, kvl - prev_key0, 128);
+            if (prev_key0 < dead_lo && prev_key0 + 128 > dead_sk)
+              zero_rows(sKV + stv * C::TILE, PART, C::PARTS, dead_sk > prev_key0 ? dead_sk - prev_key0 : 0,
+                        dead_lo - prev_key0 < 128 ? dead_lo - prev_key0 : 128);
+            if (first && items >= 1 &&
+                !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items - 1) & 1, abort_flag, a.status, cap)) {
               ok = false;
               break;
             }
-            if (!mbar_wait_warp(&ctl->p_full[t], (uint32_t)(cnt[t] - 1) & 1, abort_flag, a.status, cap)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t vd = umma_desc_sw128(kv_base + stv * C::TILE, PART, 1024);
-              const uint32_t tO = tbase + TM_O + 128 * t, tP = tbase + TM_S + 128 * t;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tO, tP + 8 * kk, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
+            for (int h = 0; h < 2; ++h) {
+              if (!mbar_wait_warp(&ctl->p_full[t][h], (cnt - 1) & 1, abort_flag, a.status, cap)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t vd = umma_desc_sw128(v_at, PART, 1024);
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
+                  const uint32_t tP = tS + 64 * h + 8 * (kk - 4 * h);
+                  mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first && kk == 0 ? 0u : 1u);
+                  if (!DUAL) mma_ts(tO, tP + 32, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
+                }
+                if (h == 0) mma_commit(&ctl->pv_half[t]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
-            first[t] = false;
+            if (!ok) break;
+            first = false;
           }
-          if (j < it.j1 && active(a, it, t, j)) {
-            if (elect_one()) {
-              const uint64_t qd = umma_desc_sw128(q_base + (a.dual ? t : 0) * C::TILE, 16, 1024);
-              const uint64_t kd = umma_desc_sw128(kv_base + stk * C::TILE, 16, 1024);
+          if (elect_one()) mma_commit(&ctl->kv_empty[stv]);
+          __syncwarp();
+        }
+        if (j < j1) {
+          if (!mbar_wait_warp(&ctl->kv_full[stk], (uint32_t)(sk / C::NST) & 1, abort_flag, a.status, cap)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            if (now) {
+              const uint64_t qd = umma_desc_sw128(qt, 16, 1024), kd = umma_desc_sw128(k_at, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * PART + (kk & 3) * 32) >> 4;
-                mma_ss(tbase + TM_S + 128 * t, qd + off, kd + off, C::IDESC_S, kk ? 1u : 0u);
+                mma_ss(tS, qd + off, kd + off, C::IDESC_S, kk ? 1u : 0u);
               }
               mma_commit(&ctl->s_full[t]);
             }
-            __syncwarp();
-            ++cnt[t];
+            mma_commit(&ctl->kv_empty[stk]);
+            if (j == j1 - 1) mma_commit(&ctl->q_empty);
           }
+          __syncwarp();
+          if (now) ++cnt;
+        } else if (!first) {
+          if (elect_one()) mma_commit(&ctl->o_full[t]);
+          __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) {
-          if (j > it.j0) mma_commit(&ctl->kv_empty[stv]);
-          if (j < it.j1) mma_commit(&ctl->kv_empty[stk]);
-          if (j == it.j1 - 1) mma_commit(&ctl->q_empty);
-          if (j == it.j1) {
-            if (!first[0]) mma_commit(&ctl->o_full[0]);
-            if (!first[1]) mma_commit(&ctl->o_full[1]);
-          }
-        }
-        __syncwarp();
+        prev = now;
+        prev_key0 = 128 * kt;
       }
-      if (!first[0]) ++items[0];
-      if (!first[1]) ++items[1];
-      seq += 2ll * (it.j1 - it.j0);
+      if (!first) ++items;
+      seq += 2ll * (j1 - j0);
     }
     // every MMA issued has completed before TMEM is freed
     if (elect_one()) {
@@ -417,74 +482,112 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp >= SW0) {
     // ------------------------------------------------------------ softmax
+    constexpr bool TWO = !DUAL;      // P as two bf16
     const int t = (warp - SW0) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tbase + TM_S + 128 * t + lane_off, tO = tbase + TM_O + 128 * t + lane_off;
+    uint8_t* stage = sOut + (warp - SW0) * OUT_STAGE;
     const float sl2 = g.scale * 1.4426950408889634f;
-    const int prow = a.tokens * a.pack;          // rows of a part
-    long long cnt = 0;
+    const int prow = a.tokens * a.pack;          // rows of a tile
+    uint32_t cnt = 0, meets = 0;
     int items = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item it = item_of(a, idx);
-      const int i = (it.tile + (a.dual ? t : 0)) * a.tokens + r / a.pack;     // query
-      const int head = it.hk * g.G + it.g0 + r % a.pack;
-      const bool valid = r < a.tokens * a.pack && i < it.seq.ql;
+    for (int n = 0; ok; ++n) {
+      const int ib = n % ITEMS;
+      if (!mbar_wait(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item& si = ctl->item[ib];
+      const int idx = si.idx, j0 = si.j0, j1 = si.j1, ns = si.ns, t_lo = si.t_lo, split = si.split;
+      const int batch = si.b, head0 = si.hk * g.G + si.g0, tok0 = (si.tile + (DUAL ? t : 0)) * a.tokens;
+      const Seq seq = si.seq;
+      const Turn<DUAL> turn(si, t);
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      if (idx < 0) break;
+      const int i = tok0 + (a.pack == 1 ? r : r / a.pack);                    // query
+      const int head = head0 + (a.pack == 1 ? 0 : r % a.pack);
+      const bool valid = r < prow && i < seq.ql;
       // rows that are not stored count as seeing everything: no mask for them
-      const Span sp = valid ? span_of(g, it.seq, i) : Span{0, 0x7fffffff, 0};
+      const Span sp = valid ? span_of(g, seq, i) : Span{0, 0x7fffffff, 0x7fffffff};
+      const int hi_min = (int)__reduce_min_sync(0xffffffffu, (unsigned)sp.hi);
+      const int lo_max = (int)__reduce_max_sync(0xffffffffu, (unsigned)sp.lo);
+      const int sk_min = (int)__reduce_min_sync(0xffffffffu, (unsigned)sp.sk);
       const bool warp_on = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;
-      bool any = false;
-      for (int j = it.j0; j < it.j1; ++j) {
-        if (!active(a, it, t, j)) continue;
-        if (!mbar_wait(&ctl->s_full[t], (uint32_t)cnt & 1, abort_flag, a.status, cap)) {
+      bool any = false, unset = true;
+      for (int j = j0; j < j1; ++j) {
+        const int kt = j < ns ? j : t_lo + j - ns;
+        if (!turn.on(j, kt)) continue;
+        if (!mbar_wait(&ctl->s_full[t], cnt & 1, abort_flag, a.status, cap)) {
           ok = false;
           break;
         }
         tc_fence_after();
         any = true;
-        ++cnt;
         if (warp_on) {
-          const int key0 = it.key0(j);
-          const bool full = !valid || (key0 + 128 <= sp.hi && (key0 >= sp.lo || key0 + 128 <= sp.sk));
-          const bool masked = __any_sync(0xffffffffu, !full);
-          if (__any_sync(0xffffffffu, m == -INFINITY)) {
-            const float mx = row_max(tS, sp, key0) * sl2;
-            if (m == -INFINITY) m = mx;
-          }
-          uint32_t pk[64];
-          const float m_use = m == -INFINITY ? 0.f : m;
-          float sum = masked ? exp_row<true>(tS, sl2, m_use, sp, key0, pk) : exp_row<false>(tS, sl2, m_use, sp, key0, pk);
-          const bool over = valid && !(sum <= RESCALE_SUM);
-          if (__any_sync(0xffffffffu, over)) {
-            // too large (or not a number): move the reference up; every MMA
-            // before this S is complete, so O holds the earlier steps
-            const float mx = fmaxf(row_max(tS, sp, key0) * sl2, m_use);
-            const float m_new = over ? mx : m_use;
-            const float alpha = ex2(m_use - m_new);
-            if (over) m = m_new;
-            sum = exp_row<true>(tS, sl2, m_new, sp, key0, pk);
-            if (__any_sync(0xffffffffu, over && l > 0.f)) {
-#pragma unroll 1
-              for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t o[32];
-                tmem_ld32(tO + ch * 32, o);
-                tmem_wait_ld();
+          const int key0 = 128 * kt;
+          const bool masked = !(key0 + 128 <= hi_min && (key0 >= lo_max || key0 + 128 <= sk_min));
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                tmem_st32(tO + ch * 32, o);
-              }
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s0[32], s1[32];
+            tmem_ld32(tS + 64 * h, s0);
+            tmem_ld32(tS + 64 * h + 32, s1);
+            tmem_wait_ld();
+            const int k0 = key0 + 64 * h;
+            if (unset) {                         // some row has met no visible key yet
+              const float mx = max_half(s0, s1, sp, k0) * sl2;
+              if (m == -INFINITY) m = mx;
+              unset = __any_sync(0xffffffffu, m == -INFINITY);
             }
-            l *= alpha;
-          }
-          l += sum;
+            uint32_t pk[32], lo[TWO ? 32 : 1];
+            float m_use = m == -INFINITY ? 0.f : m;
+            float sum = masked ? exp_half<true, TWO>(s0, s1, sl2, m_use, sp, k0, pk, lo)
+                               : exp_half<false, TWO>(s0, s1, sl2, m_use, sp, k0, pk, lo);
+            const bool over = valid && !(sum <= RESCALE_SUM);
+            if (__any_sync(0xffffffffu, over)) {
+              // too large (or not a number): move the reference up and do the
+              // half again.  Before the first half every earlier MMA of the
+              // tile is complete (so says S); before the second, the first
+              // half's PV has to be.
+              tmem_ld32(tS + 64 * h, s0);
+              tmem_ld32(tS + 64 * h + 32, s1);
+              tmem_wait_ld();
+              const float mx = fmaxf(max_half(s0, s1, sp, k0) * sl2, m_use);
+              const float m_new = over ? mx : m_use;
+              const float alpha = ex2(m_use - m_new);
+              if (over) m = m_new;
+              sum = exp_half<true, TWO>(s0, s1, sl2, m_new, sp, k0, pk, lo);
+              if (__any_sync(0xffffffffu, over && l > 0.f)) {
+                if (h == 1 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                  uint32_t o[32];
+                  tmem_ld32(tO + ch * 32, o);
+                  tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, pk + 16 * c);
-          tmem_wait_st();
+                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                  tmem_st32(tO + ch * 32, o);
+                }
+              }
+              l *= alpha;
+            }
+            l += sum;
+            tmem_st32(tS + 64 * h, pk);
+            if constexpr (TWO) tmem_st32(tS + 64 * h + 32, lo);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive_warp(&ctl->p_full[t][h]);
+          }
+          if (!ok) break;
+        } else {
+          tc_fence_before();
+          mbar_arrive_warp(&ctl->p_full[t][0]);
+          mbar_arrive_warp(&ctl->p_full[t][1]);
         }
-        tc_fence_before();
-        mbar_arrive_warp(&ctl->p_full[t]);
+        ++cnt;
       }
       if (!ok) break;
       // ---- epilogue
@@ -497,46 +600,50 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float lse2 = l > 0.f || l != l ? m + __log2f(l) : -INFINITY;
       const bool parts = a.parts > 1;
       const long long slot = parts ? ((long long)idx * 2 + t) * prow + r : 0;
-      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + (long long)it.b * a.o_batch +
-                            (long long)head * a.o_head + (long long)i * a.o_token;
       if (warp_on) {
+        uint8_t* row_ptr =
+            parts ? reinterpret_cast<uint8_t*>(a.part_o + slot * D)
+                  : reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
+                                               (long long)head * a.o_head + (long long)i * a.o_token);
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t o0[32], o1[32];
           if (any) {
-            tmem_ld32(tO + ch * 32, o);
+            tmem_ld32(tO + ch * 64, o0);
+            tmem_ld32(tO + ch * 64 + 32, o1);
             tmem_wait_ld();
           }
-          if (!any || inv == 0.f) {
+          const bool none = !any || inv == 0.f;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0u;
+          for (int x = 0; x < 32; ++x) {
+            o0[x] = none ? 0u : __float_as_uint(__uint_as_float(o0[x]) * inv);
+            o1[x] = none ? 0u : __float_as_uint(__uint_as_float(o1[x]) * inv);
           }
-          if (valid) {
-            if (parts) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + ch * 32);
+          if (parts) {
+            store_rows(stage, o0, row_ptr + ch * 256, valid);
+            store_rows(stage, o1, row_ptr + ch * 256 + 128, valid);
+          } else {
+            uint32_t w[32];
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                dst[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
-                                     __uint_as_float(o[4 * x + 2]) * inv, __uint_as_float(o[4 * x + 3]) * inv);
-            } else {
-              uint32_t w[16];
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                w[x] = cvt_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
-              uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            for (int x = 0; x < 16; ++x) {
+              w[x] = cvt_bf16x2(__uint_as_float(o0[2 * x]), __uint_as_float(o0[2 * x + 1]));
+              w[16 + x] = cvt_bf16x2(__uint_as_float(o1[2 * x]), __uint_as_float(o1[2 * x + 1]));
             }
+            if (ch == D / 64 - 1 && any) {       // O is in registers: the next item's first PV may overwrite it
+              tc_fence_before();
+              mbar_arrive_warp(&ctl->o_empty[t]);
+            }
+            store_rows(stage, w, row_ptr + ch * 128, valid);
           }
         }
         if (valid) {
           if (parts)
             a.part_lse[slot] = lse2;
           else
-            a.lse[((long long)it.b * g.H + head) * g.Nq + i] = lse2 * 0.6931471805599453f;
+            a.lse[((long long)batch * g.H + head) * g.Nq + i] = lse2 * 0.6931471805599453f;
         }
       }
-      if (any) {
+      if (any && (parts || !warp_on)) {
         tc_fence_before();
         mbar_arrive_warp(&ctl->o_empty[t]);
       }
@@ -544,50 +651,68 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the group that completes the query tile's parts joins them
         __threadfence();
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait(&ctl->group[t], 0u, abort_flag, a.status, cap)) break;
-        const int base = idx - it.split;               // split 0 of this item
+        if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+        const int base = idx - split;                  // split 0 of this item
         if (r == 0)
-          ctl->last[t] = atomicAdd(a.counters + (a.dual ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts - 1;
+          ctl->last[t] = atomicAdd(a.counters + (DUAL ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts - 1;
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait(&ctl->group[t], 1u, abort_flag, a.status, cap)) break;
+        if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
         if (ctl->last[t]) {
           __threadfence();
-          const int rows_tok = it.seq.ql - (it.tile + (a.dual ? t : 0)) * a.tokens;
-          const int rows = (rows_tok < a.tokens ? rows_tok : a.tokens) * a.pack;
-          constexpr int TPR = D / 4;                   // threads per row, four dims each
-          const int sub = r / TPR, d0 = (r % TPR) * 4;
-          for (int row = sub; row < rows; row += 128 / TPR) {
-            float M = -INFINITY;
-            for (int p = 0; p < a.parts; ++p) {
-              const long long sl = a.dual ? ((long long)(base + p) * 2 + t) * 128 + row
-                                          : ((long long)(base + (p >> 1)) * 2 + (p & 1)) * prow + row;
-              M = fmaxf(M, __ldcg(a.part_lse + sl));
-            }
+          const int left = seq.ql - tok0;
+          const int rows = (left < a.tokens ? left : a.tokens) * a.pack;
+          // part p of a row: split p of this tile, or split p / 2 of group p % 2
+          const long long row0 = (long long)base * 2 * prow + (DUAL ? t * prow : 0);
+          const long long step = (DUAL ? 2ll : 1ll) * prow;
+          if (r < rows) {
+            // each part's share of the row: 2^(lse_p - max) / sum, in the place of its lse
+            float* lp = a.part_lse + row0 + r;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+            for (int p = 0; p < a.parts; ++p) M = fmaxf(M, __ldcg(lp + p * step));
             const float M_use = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int p = 0; p < a.parts; ++p) L += ex2(__ldcg(lp + p * step) - M_use);
+            const float li = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll 4
+            for (int p = 0; p < a.parts; ++p) __stcg(lp + p * step, ex2(__ldcg(lp + p * step) - M_use) * li);
+            a.lse[((long long)batch * g.H + head) * g.Nq + i] =
+                li == 0.f ? -INFINITY : (M_use + __log2f(L)) * 0.6931471805599453f;
+          }
+          mbar_arrive_warp(&ctl->group[t]);
+          if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+          constexpr int TPR = D / 4, RPP = 128 / TPR;  // threads per row (four dims each), rows per pass
+          const int d0 = (r % TPR) * 4;
+          for (int row = r / TPR; row < rows; row += 2 * RPP) {
+            const bool two = row + RPP < rows;
+            float acc[2][4] = {};
+            const float* lp = a.part_lse + row0 + row;
+            const float* op = a.part_o + (row0 + row) * D + d0;
+            const int up = two ? RPP : 0;
 #pragma unroll 4
             for (int p = 0; p < a.parts; ++p) {
-              const long long sl = a.dual ? ((long long)(base + p) * 2 + t) * 128 + row
-                                          : ((long long)(base + (p >> 1)) * 2 + (p & 1)) * prow + row;
-              const float w = ex2(__ldcg(a.part_lse + sl) - M_use);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + sl * D + d0));
-              L += w;
-              acc[0] = fmaf(w, v.x, acc[0]);
-              acc[1] = fmaf(w, v.y, acc[1]);
-              acc[2] = fmaf(w, v.z, acc[2]);
-              acc[3] = fmaf(w, v.w, acc[3]);
+              const float w0 = __ldcg(lp + p * step), w1 = __ldcg(lp + p * step + up);
+              const float4 v0 = __ldcg(reinterpret_cast<const float4*>(op + p * step * D));
+              const float4 v1 = __ldcg(reinterpret_cast<const float4*>(op + (p * step + up) * D));
+              acc[0][0] = fmaf(w0, v0.x, acc[0][0]);
+              acc[0][1] = fmaf(w0, v0.y, acc[0][1]);
+              acc[0][2] = fmaf(w0, v0.z, acc[0][2]);
+              acc[0][3] = fmaf(w0, v0.w, acc[0][3]);
+              acc[1][0] = fmaf(w1, v1.x, acc[1][0]);
+              acc[1][1] = fmaf(w1, v1.y, acc[1][1]);
+              acc[1][2] = fmaf(w1, v1.z, acc[1][2]);
+              acc[1][3] = fmaf(w1, v1.w, acc[1][3]);
             }
-            const float li = L > 0.f || L != L ? 1.f / L : 0.f;
-            const int qi = (it.tile + (a.dual ? t : 0)) * a.tokens + row / a.pack;
-            const int hd = it.hk * g.G + it.g0 + row % a.pack;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)it.b * a.o_batch +
-                                 (long long)hd * a.o_head + (long long)qi * a.o_token + d0;
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(cvt_bf16x2(acc[0] * li, acc[1] * li), cvt_bf16x2(acc[2] * li, acc[3] * li));
-            if (r % TPR == 0)
-              a.lse[((long long)it.b * g.H + hd) * g.Nq + qi] =
-                  li == 0.f ? -INFINITY : (M_use + __log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (k == 1 && !two) break;
+              const int rr = row + k * RPP;
+              const int qi = tok0 + rr / a.pack, hd = head0 + rr % a.pack;
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
+                                   (long long)hd * a.o_head + (long long)qi * a.o_token + d0;
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(cvt_bf16x2(acc[k][0], acc[k][1]), cvt_bf16x2(acc[k][2], acc[k][3]));
+            }
           }
         }
       }
@@ -601,14 +726,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, bool DUAL>
 cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
                        int num_sms, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int grid = a.n_items < num_sms ? a.n_items : num_sms;
-  window_fwd_kernel<D><<<grid, THREADS, Cfg<D>::SMEM, s>>>(mq, mk, mv, a);
+  window_fwd_kernel<D, DUAL><<<grid, THREADS, Cfg<D>::SMEM, s>>>(mq, mk, mv, a);
   return cudaGetLastError();
 }
 
@@ -616,7 +741,11 @@ cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
 
 cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
                               int num_sms, cudaStream_t s) {
-  return a.g.D == 128 ? win::launch_fwd<128>(mq, mk, mv, a, num_sms, s) : win::launch_fwd<64>(mq, mk, mv, a, num_sms, s);
+  if (a.g.D == 128)
+    return a.dual ? win::launch_fwd<128, true>(mq, mk, mv, a, num_sms, s)
+                  : win::launch_fwd<128, false>(mq, mk, mv, a, num_sms, s);
+  return a.dual ? win::launch_fwd<64, true>(mq, mk, mv, a, num_sms, s)
+                : win::launch_fwd<64, false>(mq, mk, mv, a, num_sms, s);
 }
 
 }  // namespace fvattn
