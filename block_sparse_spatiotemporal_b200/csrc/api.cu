@@ -726,8 +726,7 @@ constexpr int kWinSms = 148;
 // all queries, and the key tiles of an item split where that shortens the
 // longest CTA's work: rounds of items over the SMs times (steps of an item +
 // what an item costs besides, in steps: 4 for an item of two query tiles, 6
-// when its parts have to be joined, 1 for few queries, whose loads run ahead
-// over item borders and whose parts are small).
+// when its parts have to be joined).
 int win_plan(const WinGeom& g, WinFwdArgs* a) {
   a->g = g;
   a->pack = g.Nq < 128 && g.G <= 128 ? g.G : 1;
@@ -748,14 +747,16 @@ int win_plan(const WinGeom& g, WinFwdArgs* a) {
   if (items > 0 && items < 8 * kWinSms) {
     int64_t best = 0;
     for (int64_t s = 1; s <= 64 && (s == 1 || s <= (a->dual ? steps / 4 : (steps + 1) / 2)); ++s) {
-      const int64_t cost = ((items * s + kWinSms - 1) / kWinSms) * ((steps + s - 1) / s + (a->dual ? (s > 1 ? 6 : 4) : 1));
+      const int64_t cost = ((items * s + kWinSms - 1) / kWinSms) * ((steps + s - 1) / s + (a->dual ? (s > 1 ? 6 : 4) : 6));
       if (s == 1 || cost < best) {
         best = cost;
         a->splits = (int)s;
       }
     }
   }
-  a->parts = a->dual ? a->splits : 2 * a->splits;
+  const int rows = a->tokens * a->pack;
+  a->copies = a->dual || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+  a->parts = a->dual ? a->splits : 2 * a->copies * a->splits;
   a->n_items = (int)(items * a->splits);
   return FVATTN_OK;
 }
@@ -769,7 +770,7 @@ WinWs win_ws(const WinFwdArgs& a) {
   L.next_item = sizeof(int);
   L.zeroed = 2 * sizeof(int);
   if (a.parts > 1) {
-    const size_t rows = (size_t)a.n_items * 2 * a.tokens * a.pack;
+    const size_t rows = (size_t)a.n_items * 2 * a.copies * a.tokens * a.pack;
     L.counters = off;
     const size_t n = sizeof(int) * (size_t)(a.n_items / a.splits) * 2;
     off = align_up(off + n);

@@ -205,13 +205,14 @@ struct WinFwdArgs {
   int pack;                        // query heads of a KV head in one tile: 1 or G
   int tokens;                      // queries of a tile
   int item_tiles;                  // items per (batch, KV head, head slot)
+  int copies;                      // of the rows in a tile, each with its share of the keys (not dual): 1, 2 or 4
   int splits, parts;               // of an item's key tiles; parts written and joined (1: none)
   int n_items;
   void* out;
   long long o_batch, o_head, o_token;
   float* lse;                      // [B, H, Nq]
-  float* part_o;                   // [n_items][2][tokens * pack][D]
-  float* part_lse;                 // [n_items][2][tokens * pack], base 2
+  float* part_o;                   // [n_items][2][copies][tokens * pack][D]
+  float* part_lse;                 // [n_items][2][copies][tokens * pack], base 2
   int* counters;                   // parts written, per item and query tile
   int* next_item;                  // zeroed: items handed out after each CTA's first
   int* status;

@@ -16,11 +16,14 @@
 //                in a ring in shared memory (the other warps would each spend
 //                3,000 clocks on its divisions), loads its Q and its K and V
 //                tiles, these through one ring;
-//   warps 1, 2   MMAs of tile A, B: per step O_g += P_g(j-1) V in two halves
-//                of 64 keys as the softmax hands them over, then
-//                S_g(j) = Q_g K^T into the TMEM columns P_g(j-1) held (MMAs
-//                of one thread run in issue order).  While one tile's softmax
-//                runs, the other's products keep the tensor cores fed;
+//   warp 1       MMAs, for tile A and then tile B of every step:
+//                O_g += P_g(j-1) V in two halves of 64 keys as the softmax
+//                hands them over, then S_g(j) = Q_g K^T into the TMEM columns
+//                P_g(j-1) held (MMAs of one thread run in issue order).  The
+//                fixed order keeps the tiles half a step apart, so that one's
+//                products run during the other's softmax; with a warp of its
+//                own for each tile both fell into step, exponentials against
+//                exponentials, and a step took 5,260 clocks instead of 4,200;
 //   warps 4-7, 8-11   softmax of tile A, B: thread r owns row r; P is
 //                written back over S as bf16 (the A operand of the PV MMA;
 //                its rounding, relative 2^-9, is the step's largest error).
@@ -32,15 +35,19 @@
 // Few queries (at most 128 rows a KV head, the query heads of a KV head
 // packed into one tile when there are fewer than 128 queries): both softmax
 // groups work on the same query tile, on alternate key tiles, and the key
-// tiles of an item are split over several CTAs.  Bound by the reading of K
+// tiles of an item are split over several CTAs.  Up to 32 (64) rows are held
+// four times (twice), 32 (64) lanes apart, and each copy's warps work on a
+// quarter (half) of every tile's keys, the rest of its P being 0: one warp
+// over all 128 keys took 4,800 clocks a tile where K and V take 2,800 to read.  Bound by the reading of K
 // and V, this form has tensor time to spare and gives P a second bf16 for
-// what the first one rounds away (a second PV product).  Each group writes
-// its normalised part and its lse to the workspace, and the last one to
+// what the first one rounds away (a second PV product).  Each copy of each group
+// writes its normalised part and its lse to the workspace, and the last one to
 // arrive (a counter per item) joins the parts in ascending order, so the
 // result does not depend on which that is.
 //
-// TMEM (512 columns): S_A, S_B at 0, 128 (each half's P over its first 32
-// columns, its second bf16 over the others), O_A, O_B at 256, 384.  Shared memory: Q 2 x
+// TMEM (512 columns): S_A, S_B at 0, 128, O_A, O_B at 256, 384.  P goes over S:
+// each 64 keys' over the first 32 of their columns, or, with its second bf16,
+// each 32 keys' two halves over their own columns.  Shared memory: Q 2 x
 // 128 rows, ring of 128-key tiles, all in 128-byte swizzled parts of 64 dims;
 // 4 KB a softmax warp for the output.
 #include "window.cuh"
@@ -81,7 +88,7 @@ struct Item {
 };
 
 struct FwdCtl {
-  uint64_t item_full[ITEMS], item_empty[ITEMS];   // 2 MMA warps and 8 softmax warps read an item
+  uint64_t item_full[ITEMS], item_empty[ITEMS];   // the MMA warp and 8 softmax warps read an item
   uint64_t q_full, q_empty;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2];      // S_g of its next step written (and every earlier MMA of the tile complete)
@@ -98,40 +105,13 @@ struct FwdCtl {
 };
 static_assert(Cfg<128>::SMEM + sizeof(FwdCtl) <= 232448 && Cfg<64>::SMEM + sizeof(FwdCtl) <= 232448, "shared memory");
 
-// Polynomial share of the exponentials: pair i of a 32-column chunk.
-#ifndef FVATTN_WIN_POLY
-#define FVATTN_WIN_POLY 1000
-#endif
-__host__ __device__ constexpr bool poly_pair(int i) { return i % FVATTN_WIN_POLY == 1 % FVATTN_WIN_POLY && FVATTN_WIN_POLY < 1000; }
-
-// 2^x of a pair on the FMA pipe: i = floor(x) from a round-down add of
-// 1.5 * 2^23, 2^(x - i) by a degree-3 polynomial (a minimax fit in relative
-// error on [0, 1), 7.5e-5, below half a bf16 step), i added to the exponent.
-__device__ inline void exp2_poly2(uint64_t X, float& y0, float& y1) {
-  constexpr float C0 = 0.9999252557754517f, C1 = 0.6958333253860474f, C2 = 0.22606715559959412f,
-                  C3 = 0.07802474498748779f, MAGIC = 12582912.f;
-  float x0, x1;
-  uf2(X, x0, x1);
-  x0 = fminf(fmaxf(x0, -126.f), 126.f);
-  x1 = fminf(fmaxf(x1, -126.f), 126.f);
-  const uint64_t C = f2(x0, x1), M = f2(MAGIC, MAGIC);
-  const uint64_t Y = add2_rm(C, M);
-  const uint64_t F = sub2(C, sub2(Y, M));
-  uint64_t P = fma2(F, f2(C3, C3), f2(C2, C2));
-  P = fma2(P, F, f2(C1, C1));
-  P = fma2(P, F, f2(C0, C0));
-  float p0, p1, q0, q1;
-  uf2(P, p0, p1);
-  uf2(Y, q0, q1);
-  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(q0) << 23));
-  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(q1) << 23));
-}
-
 // P of 32 logits as 16 bf16x2 words (and what they round away as 16 more),
-// their fp32 sum added to acc.
+// their fp32 sum added to acc.  In three sweeps: one pair after another waits
+// out every instruction's latency.
 template <bool MASKED, bool TWO>
 __device__ inline void exp_chunk(const uint32_t (&s)[32], uint64_t SL, uint64_t NM, uint32_t mask, uint32_t* pk,
                                  uint32_t* lo, uint64_t (&acc)[2]) {
+  float x[32];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float a = __uint_as_float(s[2 * i]), b = __uint_as_float(s[2 * i + 1]);
@@ -139,20 +119,16 @@ __device__ inline void exp_chunk(const uint32_t (&s)[32], uint64_t SL, uint64_t 
       a = (mask >> (2 * i)) & 1u ? a : -INFINITY;
       b = (mask >> (2 * i + 1)) & 1u ? b : -INFINITY;
     }
-    const uint64_t X = fma2(f2(a, b), SL, NM);
-    float p0, p1;
-    if (!MASKED && !TWO && poly_pair(i)) {
-      exp2_poly2(X, p0, p1);
-    } else {
-      float x0, x1;
-      uf2(X, x0, x1);
-      p0 = ex2(x0);
-      p1 = ex2(x1);
-    }
-    acc[i & 1] = add2(acc[i & 1], f2(p0, p1));
-    const uint32_t w = cvt_bf16x2(p0, p1);
+    uf2(fma2(f2(a, b), SL, NM), x[2 * i], x[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = ex2(x[i]);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    acc[i & 1] = add2(acc[i & 1], f2(x[2 * i], x[2 * i + 1]));
+    const uint32_t w = cvt_bf16x2(x[2 * i], x[2 * i + 1]);
     pk[i] = w;
-    if (TWO) lo[i] = cvt_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xFFFF0000u));
+    if (TWO) lo[i] = cvt_bf16x2(x[2 * i] - __uint_as_float(w << 16), x[2 * i + 1] - __uint_as_float(w & 0xFFFF0000u));
   }
 }
 
@@ -160,27 +136,45 @@ __device__ inline uint32_t chunk_mask(const Span& sp, int key0) {
   return bits(sp.lo - key0, sp.hi - key0) | bits(0, sp.sk - key0);
 }
 
-// P of a row's 64 logits and their sum.
-template <bool MASKED, bool TWO>
-__device__ inline float exp_half(const uint32_t (&s0)[32], const uint32_t (&s1)[32], float sl2, float m, const Span& sp,
-                                 int key0, uint32_t (&pk)[32], uint32_t (&lo)[TWO ? 32 : 1]) {
+// P of a row's 64 logits, which start at tS, and their sum.
+template <bool MASKED>
+__device__ inline float exp_half(uint32_t tS, float sl2, float m, const Span& sp, int key0, uint32_t (&pk)[32]) {
   const uint64_t SL = f2(sl2, sl2), NM = f2(-m, -m);
   uint64_t acc[2] = {0ull, 0ull};
-  exp_chunk<MASKED, TWO>(s0, SL, NM, MASKED ? chunk_mask(sp, key0) : 0u, pk, lo, acc);
-  exp_chunk<MASKED, TWO>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32) : 0u, pk + 16, TWO ? lo + 16 : lo, acc);
+  uint32_t s0[32], s1[32];
+  tmem_ld32(tS, s0);
+  tmem_wait_ld();
+  tmem_ld32(tS + 32, s1);
+  exp_chunk<MASKED, false>(s0, SL, NM, MASKED ? chunk_mask(sp, key0) : 0u, pk, nullptr, acc);
+  tmem_wait_ld();
+  exp_chunk<MASKED, false>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32) : 0u, pk + 16, nullptr, acc);
   return sum2(add2(acc[0], acc[1]));
 }
 
-// Largest visible of a row's 64 logits (-inf: none).
-__device__ inline float max_half(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const Span& sp, int key0) {
-  const uint32_t m0 = chunk_mask(sp, key0), m1 = chunk_mask(sp, key0 + 32);
+// Largest visible of a row's 32 logits at tS (-inf: none).
+__device__ inline float max_chunk(uint32_t tS, const Span& sp, int key0) {
   float m = -INFINITY;
+  uint32_t s[32];
+  tmem_ld32(tS, s);
+  tmem_wait_ld();
+  const uint32_t mask = chunk_mask(sp, key0);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if ((m0 >> i) & 1u) m = fmaxf(m, __uint_as_float(s0[i]));
-    if ((m1 >> i) & 1u) m = fmaxf(m, __uint_as_float(s1[i]));
-  }
+  for (int i = 0; i < 32; ++i)
+    if ((mask >> i) & 1u) m = fmaxf(m, __uint_as_float(s[i]));
   return m;
+}
+
+// O of this row times alpha.
+template <int D> __device__ inline void scale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int ch = 0; ch < D / 32; ++ch) {
+    uint32_t o[32];
+    tmem_ld32(tO + ch * 32, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+    tmem_st32(tO + ch * 32, o);
+  }
 }
 
 __device__ inline Item item_of(const WinFwdArgs& a, int idx0) {
@@ -265,6 +259,102 @@ __device__ inline void store_rows(uint8_t* stage, const uint32_t (&v)[32], uint8
   __syncwarp();
 }
 
+// Joining the parts of `rows` rows by 128 threads.  What other SMs wrote is
+// about 1,000 clocks away, so every step asks for several values before it
+// uses one (one after another, 24 parts of 4 rows took 25,000 clocks).
+struct JoinRows {
+  const float *lse, *o;   // part 0 of row 0
+  long long step;         // rows from a part to the next
+  int parts, rows;
+
+  // lse of rows rb .. re - 1, all parts, into sh [rows][parts]
+  __device__ void load_lse(float* sh, int rb, int re, int r) const {
+    const int n = (re - rb) * parts;
+#pragma unroll 1
+    for (int e0 = r; e0 < n; e0 += 4 * 128) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + 128 * k < n ? e0 + 128 * k : e0;
+        v[k] = __ldcg(lse + (e % parts) * step + rb + e / parts);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (e0 + 128 * k < n) sh[e0 + 128 * k] = v[k];
+    }
+  }
+  // one row's parts to their shares 2^(lse_p - max) / sum; returns its lse (natural)
+  __device__ float shares(float* sh) const {
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, sh[p]);
+    const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) {
+      const float w = ex2(sh[p] - M_use);
+      sh[p] = w;
+      L += w;
+    }
+    const float li = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) sh[p] *= li;
+    return li == 0.f ? -INFINITY : (M_use + __log2f(L)) * 0.6931471805599453f;
+  }
+  // NR rows x NP parts at a time: rows row, row + RPP, ..
+  template <int D, int NR, int NP>
+  __device__ void some(const float* sh, int rb, int re, int row, int d0, float (&acc)[NR][4]) const {
+    constexpr int RPP = 512 / D;
+    int up[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      up[k] = row + k * RPP < re ? k * RPP : 0;                // one that is not there repeats the first
+      acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+    }
+    const float* w = sh + (row - rb) * parts;
+    const float* op = o + (long long)row * D + d0;
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += NP) {
+      float4 v[NP][NR];
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
+          v[p][k] = __ldcg(reinterpret_cast<const float4*>(op + ((p0 + p < parts ? p0 + p : p0) * step + up[k]) * D));
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+          const float x = p0 + p < parts ? w[up[k] * parts + p0 + p] : 0.f;
+          acc[k][0] = fmaf(x, v[p][k].x, acc[k][0]);
+          acc[k][1] = fmaf(x, v[p][k].y, acc[k][1]);
+          acc[k][2] = fmaf(x, v[p][k].z, acc[k][2]);
+          acc[k][3] = fmaf(x, v[p][k].w, acc[k][3]);
+        }
+    }
+  }
+  // out(row, first dim, four dims) for rows rb .. re - 1
+  template <int D, typename F> __device__ void sum(const float* sh, int rb, int re, int r, F out) const {
+    constexpr int TPR = D / 4, RPP = 128 / TPR;        // threads a row, rows a pass
+    const int d0 = (r % TPR) * 4;
+    if (re - rb <= RPP) {
+      const int row = rb + r / TPR;
+      if (row >= re) return;
+      float acc[1][4];
+      some<D, 1, 8>(sh, rb, re, row, d0, acc);
+      out(row, d0, acc[0]);
+    } else {
+#pragma unroll 1
+      for (int row = rb + r / TPR; row < re; row += 4 * RPP) {
+        float acc[4][4];
+        some<D, 4, 2>(sh, rb, re, row, d0, acc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row + k * RPP < re) out(row + k * RPP, d0, acc[k]);
+      }
+    }
+  }
+};
+
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -285,13 +375,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], 10);
+      mbar_init(&ctl->item_empty[i], 9);
     }
     mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 2);
+    mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
-      mbar_init(&ctl->kv_empty[i], 2);
+      mbar_init(&ctl->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
@@ -302,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&ctl->o_empty[i], 4);
       mbar_init(&ctl->group[i], 4);
     }
-    mbar_init(&ctl->drain, 2);
+    mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -341,11 +431,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (it.j0 >= it.j1) continue;
         if (q_issued >= 1 && !mbar_wait(&ctl->q_empty, (uint32_t)(q_issued - 1) & 1, abort_flag, a.status, cap)) break;
         const int tiles = DUAL ? 2 : 1;
-        mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(tiles * C::PARTS * a.pack * a.tokens) * 128u);
+        const int copies = DUAL ? 1 : a.copies;
+        mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(tiles * copies * C::PARTS * a.pack * a.tokens) * 128u);
         for (int t = 0; t < tiles; ++t)
-          for (int h = 0; h < C::PARTS; ++h)
-            tma_load_5d(sQ + t * C::TILE + h * PART, &mq, &ctl->q_full, 64 * h, it.g0, (it.tile + t) * a.tokens, it.hk,
-                        it.b);
+          for (int c = 0; c < copies; ++c)
+            for (int h = 0; h < C::PARTS; ++h)
+              tma_load_5d(sQ + t * C::TILE + h * PART + c * (PART / copies), &mq, &ctl->q_full, 64 * h, it.g0,
+                          (it.tile + t) * a.tokens, it.hk, it.b);
         ++q_issued;
         for (int j = it.j0; j < it.j1 && ok; ++j) {
           const int key0 = 128 * it.key_tile(j);
@@ -370,58 +462,62 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(&ctl->kv_full[i], (uint32_t)(last / C::NST) & 1, a.status, cap);
       }
     }
-  } else if (warp == 1 || warp == 2) {
-    // ------------------------------------------------------- MMAs of tile t
-    const int t = warp - 1;
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
     long long seq = 0;               // ring number of the K tile of the item's first step
     int q_items = 0;                 // items with steps
-    uint32_t cnt = 0;                // steps of this tile
-    int items = 0;                   // items whose O_t was written
+    uint32_t cnt[2] = {0, 0};        // steps of each tile
+    int items[2] = {0, 0};           // items whose O_t was written
     bool ok = true;
-    const uint32_t qt = uni(smem_u32(sQ) + (DUAL ? t : 0) * C::TILE), kv_base = smem_u32(sKV);
-    const uint32_t tS = uni(tbase + TM_S + 128 * t), tO = uni(tbase + TM_O + 128 * t);
+    const uint32_t q_at = uni(smem_u32(sQ)), kv_base = smem_u32(sKV), tb = uni(tbase);
     for (int n = 0; ok; ++n) {
       const int ib = n % ITEMS;
       if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
       const Item& si = ctl->item[ib];
       const int idx = si.idx, j0 = si.j0, j1 = si.j1, ns = si.ns, t_lo = si.t_lo, kvl = si.seq.kvl;
       const int dead_lo = si.dead_lo, dead_sk = si.dead_sk;
-      const Turn<DUAL> turn(si, t);
+      const Turn<DUAL> turn[2] = {Turn<DUAL>(si, 0), Turn<DUAL>(si, 1)};
       mbar_arrive_warp(&ctl->item_empty[ib]);
       if (idx < 0) break;
       if (j0 >= j1) continue;
       if (!mbar_wait_warp(&ctl->q_full, (uint32_t)q_items & 1, abort_flag, a.status, cap)) break;
       ++q_items;
-      bool first = true, prev = false;
+      bool first[2] = {true, true}, prev[2] = {false, false};
       int prev_key0 = 0;
-      for (int j = j0; j <= j1; ++j) {
+      for (int j = j0; j <= j1 && ok; ++j) {
         const long long sk = seq + 2ll * (j - j0), sv = sk - 1;     // K of step j, V of step j - 1
         const int stk = (int)(sk % C::NST), stv = (int)(sv % C::NST);
         const uint32_t k_at = uni(kv_base + stk * C::TILE), v_at = uni(kv_base + stv * C::TILE);
         const int kt = j < ns ? j : t_lo + j - ns;
-        const bool now = j < j1 && turn.on(j, kt);
         if (j > j0) {
           if (!mbar_wait_warp(&ctl->kv_full[stv], (uint32_t)(sv / C::NST) & 1, abort_flag, a.status, cap)) {
             ok = false;
             break;
           }
-          if (prev) {
-            // values that no query of the sequence sees may be anything: their
-            // probabilities are 0, and 0 times NaN is not.  (Both tiles' warps
-            // write the same zeros before they use the tile.)
-            if (prev_key0 + 128 > kvl && kvl < g.Nk)
-              zero_rows(sKV + stv * C::TILE, PART, C::PARTS, kvl - prev_key0, 128);
-            if (prev_key0 < dead_lo && prev_key0 + 128 > dead_sk)
-              zero_rows(sKV + stv * C::TILE, PART, C::PARTS, dead_sk > prev_key0 ? dead_sk - prev_key0 : 0,
-                        dead_lo - prev_key0 < 128 ? dead_lo - prev_key0 : 128);
-            if (first && items >= 1 &&
-                !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items - 1) & 1, abort_flag, a.status, cap)) {
+          // values that no query of the sequence sees may be anything: their
+          // probabilities are 0, and 0 times NaN is not
+          if (prev_key0 + 128 > kvl && kvl < g.Nk)
+            zero_rows(sKV + stv * C::TILE, PART, C::PARTS, kvl - prev_key0, 128);
+          if (prev_key0 < dead_lo && prev_key0 + 128 > dead_sk)
+            zero_rows(sKV + stv * C::TILE, PART, C::PARTS, dead_sk > prev_key0 ? dead_sk - prev_key0 : 0,
+                      dead_lo - prev_key0 < 128 ? dead_lo - prev_key0 : 128);
+        }
+        if (j < j1 && !mbar_wait_warp(&ctl->kv_full[stk], (uint32_t)(sk / C::NST) & 1, abort_flag, a.status, cap)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t tS = tb + TM_S + 128 * t, tO = tb + TM_O + 128 * t;
+          if (prev[t]) {
+            if (first[t] && items[t] >= 1 &&
+                !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items[t] - 1) & 1, abort_flag, a.status, cap)) {
               ok = false;
               break;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait_warp(&ctl->p_full[t][h], (cnt - 1) & 1, abort_flag, a.status, cap)) {
+              if (!mbar_wait_warp(&ctl->p_full[t][h], (cnt[t] - 1) & 1, abort_flag, a.status, cap)) {
                 ok = false;
                 break;
               }
@@ -430,28 +526,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint64_t vd = umma_desc_sw128(v_at, PART, 1024);
 #pragma unroll
                 for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
-                  const uint32_t tP = tS + 64 * h + 8 * (kk - 4 * h);
-                  mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first && kk == 0 ? 0u : 1u);
-                  if (!DUAL) mma_ts(tO, tP + 32, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
+                  const uint32_t tP = DUAL ? tS + 64 * h + 8 * (kk - 4 * h) : tS + 32 * (kk >> 1) + 8 * (kk & 1);
+                  mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
+                  if (!DUAL) mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
                 }
                 if (h == 0) mma_commit(&ctl->pv_half[t]);
+                if (h == 1 && j == j1) mma_commit(&ctl->o_full[t]);
               }
               __syncwarp();
             }
             if (!ok) break;
-            first = false;
+            first[t] = false;
+          } else if (j == j1 && !first[t]) {     // its last PV was an earlier step's
+            if (elect_one()) mma_commit(&ctl->o_full[t]);
+            __syncwarp();
           }
-          if (elect_one()) mma_commit(&ctl->kv_empty[stv]);
-          __syncwarp();
-        }
-        if (j < j1) {
-          if (!mbar_wait_warp(&ctl->kv_full[stk], (uint32_t)(sk / C::NST) & 1, abort_flag, a.status, cap)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            if (now) {
-              const uint64_t qd = umma_desc_sw128(qt, 16, 1024), kd = umma_desc_sw128(k_at, 16, 1024);
+          prev[t] = j < j1 && turn[t].on(j, kt);
+          if (prev[t]) {
+            if (elect_one()) {
+              const uint64_t qd = umma_desc_sw128(q_at + (DUAL ? t : 0) * C::TILE, 16, 1024);
+              const uint64_t kd = umma_desc_sw128(k_at, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * PART + (kk & 3) * 32) >> 4;
@@ -459,19 +553,21 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
               mma_commit(&ctl->s_full[t]);
             }
-            mma_commit(&ctl->kv_empty[stk]);
-            if (j == j1 - 1) mma_commit(&ctl->q_empty);
+            __syncwarp();
+            ++cnt[t];
           }
-          __syncwarp();
-          if (now) ++cnt;
-        } else if (!first) {
-          if (elect_one()) mma_commit(&ctl->o_full[t]);
-          __syncwarp();
         }
-        prev = now;
+        if (!ok) break;
+        if (elect_one()) {
+          if (j > j0) mma_commit(&ctl->kv_empty[stv]);
+          if (j < j1) mma_commit(&ctl->kv_empty[stk]);
+          if (j == j1 - 1) mma_commit(&ctl->q_empty);
+        }
+        __syncwarp();
         prev_key0 = 128 * kt;
       }
-      if (!first) ++items;
+      items[0] += !first[0];
+      items[1] += !first[1];
       seq += 2ll * (j1 - j0);
     }
     // every MMA issued has completed before TMEM is freed
@@ -482,7 +578,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp >= SW0) {
     // ------------------------------------------------------------ softmax
-    constexpr bool TWO = !DUAL;      // P as two bf16
     const int t = (warp - SW0) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -490,6 +585,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* stage = sOut + (warp - SW0) * OUT_STAGE;
     const float sl2 = g.scale * 1.4426950408889634f;
     const int prow = a.tokens * a.pack;          // rows of a tile
+    // Single form with few rows: every 128 / copies lanes hold a copy of the
+    // rows, and each copy works on its share of the tile's 32-key chunks.
+    const int copies = DUAL ? 1 : a.copies;
+    const int copy = r / (128 / copies), rl = r % (128 / copies);
+    const uint32_t chunks = ((1u << (4 / copies)) - 1u) << (copy * (4 / copies));
     uint32_t cnt = 0, meets = 0;
     int items = 0;
     bool ok = true;
@@ -503,9 +603,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Turn<DUAL> turn(si, t);
       mbar_arrive_warp(&ctl->item_empty[ib]);
       if (idx < 0) break;
-      const int i = tok0 + (a.pack == 1 ? r : r / a.pack);                    // query
-      const int head = head0 + (a.pack == 1 ? 0 : r % a.pack);
-      const bool valid = r < prow && i < seq.ql;
+      const int i = tok0 + (a.pack == 1 ? rl : rl / a.pack);                  // query
+      const int head = head0 + (a.pack == 1 ? 0 : rl % a.pack);
+      const bool valid = rl < prow && i < seq.ql;
       // rows that are not stored count as seeing everything: no mask for them
       const Span sp = valid ? span_of(g, seq, i) : Span{0, 0x7fffffff, 0x7fffffff};
       const int hi_min = (int)__reduce_min_sync(0xffffffffu, (unsigned)sp.hi);
@@ -526,60 +626,108 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp_on) {
           const int key0 = 128 * kt;
           const bool masked = !(key0 + 128 <= hi_min && (key0 >= lo_max || key0 + 128 <= sk_min));
+          if constexpr (DUAL) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s0[32], s1[32];
-            tmem_ld32(tS + 64 * h, s0);
-            tmem_ld32(tS + 64 * h + 32, s1);
-            tmem_wait_ld();
-            const int k0 = key0 + 64 * h;
-            if (unset) {                         // some row has met no visible key yet
-              const float mx = max_half(s0, s1, sp, k0) * sl2;
-              if (m == -INFINITY) m = mx;
-              unset = __any_sync(0xffffffffu, m == -INFINITY);
-            }
-            uint32_t pk[32], lo[TWO ? 32 : 1];
-            float m_use = m == -INFINITY ? 0.f : m;
-            float sum = masked ? exp_half<true, TWO>(s0, s1, sl2, m_use, sp, k0, pk, lo)
-                               : exp_half<false, TWO>(s0, s1, sl2, m_use, sp, k0, pk, lo);
-            const bool over = valid && !(sum <= RESCALE_SUM);
-            if (__any_sync(0xffffffffu, over)) {
-              // too large (or not a number): move the reference up and do the
-              // half again.  Before the first half every earlier MMA of the
-              // tile is complete (so says S); before the second, the first
-              // half's PV has to be.
-              tmem_ld32(tS + 64 * h, s0);
-              tmem_ld32(tS + 64 * h + 32, s1);
-              tmem_wait_ld();
-              const float mx = fmaxf(max_half(s0, s1, sp, k0) * sl2, m_use);
-              const float m_new = over ? mx : m_use;
-              const float alpha = ex2(m_use - m_new);
-              if (over) m = m_new;
-              sum = exp_half<true, TWO>(s0, s1, sl2, m_new, sp, k0, pk, lo);
-              if (__any_sync(0xffffffffu, over && l > 0.f)) {
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t tH = tS + 64 * h;
+              const int k0 = key0 + 64 * h;
+              if (unset) {                       // some row has met no visible key yet
+                const float mx = fmaxf(max_chunk(tH, sp, k0), max_chunk(tH + 32, sp, k0 + 32)) * sl2;
+                if (m == -INFINITY) m = mx;
+                unset = __any_sync(0xffffffffu, m == -INFINITY);
+              }
+              uint32_t pk[32];
+              const float m_use = m == -INFINITY ? 0.f : m;
+              float sum = masked ? exp_half<true>(tH, sl2, m_use, sp, k0, pk) : exp_half<false>(tH, sl2, m_use, sp, k0, pk);
+              const bool over = valid && !(sum <= RESCALE_SUM);
+              if (__any_sync(0xffffffffu, over)) {
+                // too large (or not a number): move the reference up and do
+                // the half again.  Before the first half every earlier MMA of
+                // the tile is complete (so says S); before the second, the
+                // first half's PV has to be.
+                const float mx = fmaxf(fmaxf(max_chunk(tH, sp, k0), max_chunk(tH + 32, sp, k0 + 32)) * sl2, m_use);
+                const float m_new = over ? mx : m_use;
+                const float alpha = ex2(m_use - m_new);
+                if (over) m = m_new;
+                sum = exp_half<true>(tH, sl2, m_new, sp, k0, pk);
                 if (h == 1 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
                   ok = false;
                   break;
                 }
                 tc_fence_after();
-#pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                  uint32_t o[32];
-                  tmem_ld32(tO + ch * 32, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                  tmem_st32(tO + ch * 32, o);
-                }
+                scale_o<D>(tO, alpha);           // before an item's first PV it holds nothing that is used
+                l *= alpha;
               }
-              l *= alpha;
+              l += sum;
+              tmem_st32(tH, pk);
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive_warp(&ctl->p_full[t][h]);
             }
-            l += sum;
-            tmem_st32(tS + 64 * h, pk);
-            if constexpr (TWO) tmem_st32(tS + 64 * h + 32, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive_warp(&ctl->p_full[t][h]);
+          } else {
+            // 32 keys at a time, P as two bf16 in the columns of their logits
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t tC = tS + 32 * c;
+              uint32_t pk[32];
+              if ((chunks >> c) & 1u) {
+                const int k0 = key0 + 32 * c;
+                if (unset) {
+                  const float mx = max_chunk(tC, sp, k0) * sl2;
+                  if (m == -INFINITY) m = mx;
+                  unset = __any_sync(0xffffffffu, m == -INFINITY);
+                }
+                float m_use = m == -INFINITY ? 0.f : m;
+                float sum;
+#pragma unroll 1
+                for (int again = 0;; ++again) {
+                  uint32_t s[32];
+                  uint64_t acc[2] = {0ull, 0ull};
+                  tmem_ld32(tC, s);
+                  tmem_wait_ld();
+                  exp_chunk<true, true>(s, f2(sl2, sl2), f2(-m_use, -m_use), masked ? chunk_mask(sp, k0) : ~0u, pk, pk + 16,
+                                        acc);
+                  sum = sum2(add2(acc[0], acc[1]));
+                  const bool over = again == 0 && valid && !(sum <= RESCALE_SUM);
+                  if (!__any_sync(0xffffffffu, over)) break;
+                  // as above; what this half already holds of P moves too
+                  const float m_new = over ? fmaxf(max_chunk(tC, sp, k0) * sl2, m_use) : m_use;
+                  const float alpha = ex2(m_use - m_new);
+                  if (over) m = m_new;
+                  m_use = m_new;
+                  if (c >= 2 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                  scale_o<D>(tO, alpha);
+                  l *= alpha;
+                  if ((c & 1) && ((chunks >> (c - 1)) & 1u)) {
+                    tmem_ld32(tC - 32, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                      const float p0 = (__uint_as_float(s[x] << 16) + __uint_as_float(s[16 + x] << 16)) * alpha;
+                      const float p1 = (__uint_as_float(s[x] & 0xFFFF0000u) + __uint_as_float(s[16 + x] & 0xFFFF0000u)) * alpha;
+                      s[x] = cvt_bf16x2(p0, p1);
+                      s[16 + x] = cvt_bf16x2(p0 - __uint_as_float(s[x] << 16), p1 - __uint_as_float(s[x] & 0xFFFF0000u));
+                    }
+                    tmem_st32(tC - 32, s);
+                  }
+                }
+                if (!ok) break;
+                l += sum;
+              } else {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) pk[x] = 0u;
+              }
+              tmem_st32(tC, pk);
+              if (c & 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive_warp(&ctl->p_full[t][c >> 1]);
+              }
+            }
           }
           if (!ok) break;
         } else {
@@ -598,8 +746,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const float lse2 = l > 0.f || l != l ? m + __log2f(l) : -INFINITY;
-      const bool parts = a.parts > 1;
-      const long long slot = parts ? ((long long)idx * 2 + t) * prow + r : 0;
+      const bool parts = !DUAL || a.parts > 1;
+      const long long slot = parts ? (((long long)idx * 2 + t) * copies + copy) * prow + rl : 0;
       if (warp_on) {
         uint8_t* row_ptr =
             parts ? reinterpret_cast<uint8_t*>(a.part_o + slot * D)
@@ -619,7 +767,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             o0[x] = none ? 0u : __float_as_uint(__uint_as_float(o0[x]) * inv);
             o1[x] = none ? 0u : __float_as_uint(__uint_as_float(o1[x]) * inv);
           }
-          if (parts) {
+          if (!DUAL) {
+            if (valid) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                reinterpret_cast<uint4*>(row_ptr + ch * 256)[x] = make_uint4(o0[4 * x], o0[4 * x + 1], o0[4 * x + 2], o0[4 * x + 3]);
+                reinterpret_cast<uint4*>(row_ptr + ch * 256 + 128)[x] = make_uint4(o1[4 * x], o1[4 * x + 1], o1[4 * x + 2], o1[4 * x + 3]);
+              }
+            }
+          } else if (parts) {
             store_rows(stage, o0, row_ptr + ch * 256, valid);
             store_rows(stage, o1, row_ptr + ch * 256 + 128, valid);
           } else {
@@ -654,66 +810,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
         const int base = idx - split;                  // split 0 of this item
         if (r == 0)
-          ctl->last[t] = atomicAdd(a.counters + (DUAL ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts - 1;
+          ctl->last[t] = atomicAdd(a.counters + (DUAL ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts / copies - 1;
         mbar_arrive_warp(&ctl->group[t]);
         if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
         if (ctl->last[t]) {
           __threadfence();
           const int left = seq.ql - tok0;
           const int rows = (left < a.tokens ? left : a.tokens) * a.pack;
-          // part p of a row: split p of this tile, or split p / 2 of group p % 2
-          const long long row0 = (long long)base * 2 * prow + (DUAL ? t * prow : 0);
+          // part p of a row: split p of this tile, or copy p % copies of group (p / copies) % 2 of its split
+          const long long row0 = (long long)base * 2 * copies * prow + (DUAL ? t * prow : 0);
           const long long step = (DUAL ? 2ll : 1ll) * prow;
-          if (r < rows) {
-            // each part's share of the row: 2^(lse_p - max) / sum, in the place of its lse
-            float* lp = a.part_lse + row0 + r;
-            float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-            for (int p = 0; p < a.parts; ++p) M = fmaxf(M, __ldcg(lp + p * step));
-            const float M_use = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-            for (int p = 0; p < a.parts; ++p) L += ex2(__ldcg(lp + p * step) - M_use);
-            const float li = L > 0.f || L != L ? 1.f / L : 0.f;
-#pragma unroll 4
-            for (int p = 0; p < a.parts; ++p) __stcg(lp + p * step, ex2(__ldcg(lp + p * step) - M_use) * li);
-            a.lse[((long long)batch * g.H + head) * g.Nq + i] =
-                li == 0.f ? -INFINITY : (M_use + __log2f(L)) * 0.6931471805599453f;
-          }
-          mbar_arrive_warp(&ctl->group[t]);
-          if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
-          constexpr int TPR = D / 4, RPP = 128 / TPR;  // threads per row (four dims each), rows per pass
-          const int d0 = (r % TPR) * 4;
-          for (int row = r / TPR; row < rows; row += 2 * RPP) {
-            const bool two = row + RPP < rows;
-            float acc[2][4] = {};
-            const float* lp = a.part_lse + row0 + row;
-            const float* op = a.part_o + (row0 + row) * D + d0;
-            const int up = two ? RPP : 0;
-#pragma unroll 4
-            for (int p = 0; p < a.parts; ++p) {
-              const float w0 = __ldcg(lp + p * step), w1 = __ldcg(lp + p * step + up);
-              const float4 v0 = __ldcg(reinterpret_cast<const float4*>(op + p * step * D));
-              const float4 v1 = __ldcg(reinterpret_cast<const float4*>(op + (p * step + up) * D));
-              acc[0][0] = fmaf(w0, v0.x, acc[0][0]);
-              acc[0][1] = fmaf(w0, v0.y, acc[0][1]);
-              acc[0][2] = fmaf(w0, v0.z, acc[0][2]);
-              acc[0][3] = fmaf(w0, v0.w, acc[0][3]);
-              acc[1][0] = fmaf(w1, v1.x, acc[1][0]);
-              acc[1][1] = fmaf(w1, v1.y, acc[1][1]);
-              acc[1][2] = fmaf(w1, v1.z, acc[1][2]);
-              acc[1][3] = fmaf(w1, v1.w, acc[1][3]);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if (k == 1 && !two) break;
-              const int rr = row + k * RPP;
-              const int qi = tok0 + rr / a.pack, hd = head0 + rr % a.pack;
+          const JoinRows jr{a.part_lse + row0, a.part_o + row0 * D, step, a.parts, rows};
+          float* share = reinterpret_cast<float*>(sOut + t * 4 * OUT_STAGE);        // [batch of rows][parts]
+          const int most = (int)(4 * OUT_STAGE / sizeof(float)) / a.parts;
+          bool joined = true;
+          for (int rb = 0; rb < rows && joined; rb += most) {
+            const int re = rb + most < rows ? rb + most : rows;
+            jr.load_lse(share, rb, re, r);
+            mbar_arrive_warp(&ctl->group[t]);
+            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            if (!joined) break;
+            const int row = rb + r;
+            if (row < re)
+              a.lse[((long long)batch * g.H + head0 + row % a.pack) * g.Nq + tok0 + row / a.pack] =
+                  jr.shares(share + r * a.parts);
+            mbar_arrive_warp(&ctl->group[t]);
+            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            if (!joined) break;
+            jr.template sum<D>(share, rb, re, r, [&](int rr, int d0, const float (&v)[4]) {
               __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
-                                   (long long)hd * a.o_head + (long long)qi * a.o_token + d0;
-              *reinterpret_cast<uint2*>(dst) =
-                  make_uint2(cvt_bf16x2(acc[k][0], acc[k][1]), cvt_bf16x2(acc[k][2], acc[k][3]));
-            }
+                                   (long long)(head0 + rr % a.pack) * a.o_head +
+                                   (long long)(tok0 + rr / a.pack) * a.o_token + d0;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+            });
+            mbar_arrive_warp(&ctl->group[t]);          // the shares are read
+            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
           }
+          if (!joined) break;
         }
       }
     }
