@@ -638,6 +638,10 @@ int win_geom(const fvattn_window* w, WinGeom* g) {
     return FVATTN_ERR_SHAPE;
   if (w->q_len > (1 << 28) || w->kv_len > (1 << 28) || (int64_t)w->batch * w->heads > (1 << 20)) return FVATTN_ERR_SHAPE;
   if (w->head_dim != 64 && w->head_dim != 128) return FVATTN_ERR_SHAPE;
+  // 128-row tiles of either side, counted over all heads, stay below 2^26
+  if ((int64_t)w->batch * w->heads * ((w->q_len + 127) / 128) > (1 << 26) ||
+      (int64_t)w->batch * w->kv_heads * ((w->kv_len + 127) / 128) > (1 << 26))
+    return FVATTN_ERR_SHAPE;
   if (w->unit < 1 || w->window < 0 || w->sinks < 0) return FVATTN_ERR_INVALID_ARG;
   if (std::isnan(w->scale) || w->scale < 0.f || std::isinf(w->scale)) return FVATTN_ERR_INVALID_ARG;
   *g = WinGeom{};
@@ -784,12 +788,64 @@ WinWs win_ws(const WinFwdArgs& a) {
   return L;
 }
 
-struct WinBwdWs {
-  size_t lse2, dd, total;
+// Key-stationary items of the backward: 128-key tiles, those with sinks apart,
+// and in how many parts the steps (64 queries) of either are split: the split
+// with the shortest estimate of the longest SM's work, an item counting 6
+// steps besides its own and 10 when its parts have to be added.
+struct WinBwdPlan {
+  int tiles, heavy_tiles, heavy_parts, parts, n_items;
 };
-WinBwdWs win_bwd_ws(const WinGeom& g) {
+WinBwdPlan win_bwd_plan(const WinGeom& g) {
+  WinBwdPlan p{(g.Nk + 127) / 128, 0, 1, 1, 0};
+  const int64_t sink_tiles = g.window > 0 ? ((int64_t)g.sinks * g.unit + 127) / 128 : 0;
+  p.heavy_tiles = (int)(sink_tiles < p.tiles ? sink_tiles : p.tiles);
+  const int64_t cells = (int64_t)g.B * g.Hk;
+  const int64_t q_tiles = (g.Nq + 63) / 64;
+  const int64_t n_h = g.G * q_tiles;
+  int64_t n_n = n_h;
+  if (g.window > 0) {
+    const int64_t w = ((int64_t)g.window * g.unit + 127) / 64 + 2;
+    n_n = g.G * (w < q_tiles ? w : q_tiles);
+  }
+  const int64_t items_h = cells * p.heavy_tiles, items_n = cells * (p.tiles - p.heavy_tiles);
+  double best = 0;
+  for (int k = 1; k <= 32; ++k) {
+    const int64_t most = items_h > 0 ? n_h : n_n;          // the longest tile in k parts, the others no longer
+    const int64_t len = (most + k - 1) / k;
+    if (k > 1 && len < 4) break;
+    const int64_t hp = items_h > 0 ? k : 1, np = len > 0 ? (n_n + len - 1) / len : 1;
+    const int64_t count = items_h * hp + items_n * np;
+    if (k > 1 && count > 8 * kWinSms) break;
+    auto item = [&](int64_t n, int64_t parts) { return (double)((n + parts - 1) / parts) + (parts > 1 ? 10 : 6); };
+    const double longest = items_h > 0 ? (items_n > 0 && item(n_n, np) > item(n_h, hp) ? item(n_n, np) : item(n_h, hp))
+                                       : item(n_n, np);
+    const double all = items_h * hp * item(n_h, hp) + items_n * np * item(n_n, np);
+    const double cost = count <= kWinSms ? longest : all / kWinSms + 0.5 * longest;
+    if (k == 1 || cost < best) {
+      best = cost;
+      p.heavy_parts = (int)hp;
+      p.parts = (int)(np < 1 ? 1 : np);
+    }
+  }
+  p.n_items = (int)(items_h * p.heavy_parts + items_n * p.parts);
+  return p;
+}
+
+struct WinBwdWs {
+  size_t counters, lse2, dd, part, total, zeroed;
+};
+WinBwdWs win_bwd_ws(const WinGeom& g, const WinBwdPlan& p) {
   const size_t rows = align_up(sizeof(float) * (size_t)g.B * g.H * g.Nq);
-  return WinBwdWs{kAlign, kAlign + rows, kAlign + 2 * rows};
+  const bool split = p.heavy_parts > 1 || p.parts > 1;
+  WinBwdWs L{};
+  L.counters = kAlign;               // behind the status word
+  const size_t n = split ? sizeof(int) * (size_t)g.B * g.Hk * p.tiles : 0;
+  L.zeroed = split ? L.counters + n : sizeof(int);
+  L.lse2 = align_up(L.counters + n);
+  L.dd = L.lse2 + rows;
+  L.part = L.dd + rows;
+  L.total = L.part + (split ? sizeof(float) * (size_t)p.n_items * 2 * 128 * g.D : 0);
+  return L;
 }
 
 }  // namespace
@@ -1301,7 +1357,7 @@ int fvattn_workspace_size_window_bwd(const fvattn_window* win, size_t* bytes) {
   if (!bytes) return FVATTN_ERR_INVALID_ARG;
   WinGeom g;
   FV_TRY(win_geom(win, &g));
-  *bytes = win_bwd_ws(g).total;
+  *bytes = win_bwd_ws(g, win_bwd_plan(g)).total;
   return FVATTN_OK;
 }
 
@@ -1318,17 +1374,17 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
   if ((g.Nq > 0 && !lse) || !aligned(lse, 4) || !aligned(q_lens, 4) || !aligned(kv_lens, 4))
     return FVATTN_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, kAlign)) return FVATTN_ERR_INVALID_ARG;
-  const int q_tiles = (g.Nq + 127) / 128, k_tiles = (g.Nk + 127) / 128;
-  if ((int64_t)g.B * g.H * q_tiles > (1 << 28) || (int64_t)g.B * g.Hk * k_tiles > (1 << 28)) return FVATTN_ERR_SHAPE;
+  const int q_tiles = (g.Nq + 127) / 128;
   g.q_lens = q_lens;
   g.kv_lens = kv_lens;
-  const WinBwdWs L = win_bwd_ws(g);
+  const WinBwdPlan plan = win_bwd_plan(g);
+  const WinBwdWs L = win_bwd_ws(g, plan);
   if (ws_bytes < L.total) return FVATTN_ERR_WORKSPACE;
   DeviceInfo dev;
   FV_TRY(device_info(&dev));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
-  FV_CUDA(cudaMemsetAsync(base, 0, sizeof(int), s));
+  FV_CUDA(cudaMemsetAsync(base, 0, L.zeroed, s));
   if (g.Nq == 0 && g.Nk == 0) return FVATTN_OK;
   // a tensor without rows has no address: its maps, which no load uses, take another's
   const void* any = g.Nq > 0 ? q->data : k->data;
@@ -1352,10 +1408,13 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     FV_TRY(make_head_map(&m1, *v, g, g.Hk, g.Nk, 128, any));
     FV_TRY(make_head_map(&m2, *q, g, g.H, g.Nq, 64, any));
     FV_TRY(make_head_map(&m3, *dout, g, g.H, g.Nq, 64, any));
-    a.tiles = k_tiles;
-    a.n_items = g.B * g.Hk * k_tiles;
-    const int64_t sink_tiles = g.window > 0 ? ((int64_t)g.sinks * g.unit + 127) / 128 : 0;
-    a.heavy_tiles = (int)(sink_tiles < k_tiles ? sink_tiles : k_tiles);
+    a.tiles = plan.tiles;
+    a.heavy_tiles = plan.heavy_tiles;
+    a.heavy_parts = plan.heavy_parts;
+    a.parts = plan.parts;
+    a.n_items = plan.n_items;
+    a.part = reinterpret_cast<float*>(base + L.part);
+    a.counters = reinterpret_cast<int*>(base + L.counters);
     a.out0 = WinOut{dk->data, dk->batch, dk->head, dk->token};
     a.out1 = WinOut{dv->data, dv->batch, dv->head, dv->token};
     StageTimer t(FVATTN_STAGE_WINDOW_KV, s);
@@ -1369,7 +1428,6 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     FV_TRY(make_head_map(&m3, *v, g, g.Hk, g.Nk, 64, any));
     a.tiles = q_tiles;
     a.n_items = g.B * g.H * q_tiles;
-    a.heavy_tiles = 0;
     a.out0 = WinOut{dq->data, dq->batch, dq->head, dq->token};
     StageTimer t(FVATTN_STAGE_WINDOW_Q, s);
     FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, false, dev.sms, s));

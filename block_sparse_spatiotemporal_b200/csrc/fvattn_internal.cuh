@@ -228,6 +228,9 @@ struct WinBwdArgs {
   WinGeom g;
   int tiles;                       // 128-row stationary tiles of a (batch, head)
   int heavy_tiles;                 // key-stationary: tiles that hold sinks, run first
+  int heavy_parts, parts;          //   parts of the steps of one of them, of another tile
+  float* part;                     //   [n_items][2][128][D] sums of the parts
+  int* counters;                   //   parts written, per (batch, KV head, tile), zeroed
   int n_items;
   const float* lse2;               // [B, H, Nq] lse * log2(e)
   const float* dd;                 // [B, H, Nq] rowsum(dout * out)

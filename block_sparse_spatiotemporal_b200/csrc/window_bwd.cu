@@ -20,6 +20,11 @@
 // of the next products), and a fourth warp's accumulating MMAs read them from
 // TMEM as the A operand.  The moving tiles are used twice: K-major for the
 // scores, MN-major for the accumulations.
+// Where one tile's steps would outlast the others' (the tile of the sinks,
+// which every query sees; few KV heads under many query heads) they are split:
+// each part writes fp32 sums to the workspace, and the last one to arrive adds
+// them in ascending order (2 x 14 heads over 2 KV heads, 1,531 tokens, window
+// 300: 197 us unsplit).
 #include "window.cuh"
 
 namespace fvattn {
@@ -61,11 +66,13 @@ struct Ctl {
   uint64_t step_done[MAXNB]; // the accumulating MMAs of step c, which read buffer c % NB, complete
   uint64_t acc_full;         // the item's accumulators complete
   uint64_t acc_empty;        // the epilogue read them (8 warps)
+  uint64_t meet;             // the compute warps meet (8 warps)
   uint64_t drain;
   float lse2[MAXST][64];     // key-stationary only: lse * log2(e) of the step's queries
   float dd[MAXST][64];       //   and their rowsum(dout * out)
   uint32_t tmem_base;
   int abort;
+  int last;                  // this part was its tile's last
 };
 static_assert(Sh<128>::SMEM + sizeof(Ctl) <= 232448 && Sh<64>::SMEM + sizeof(Ctl) <= 232448, "shared memory");
 
@@ -75,6 +82,8 @@ template <bool KV> struct Item {
   int row0;              // first stationary row (key or query)
   Seq seq;
   int lo, n_per, n;      // KV: first query tile, tiles per head, steps (n_per * G)
+  int j0, j1;            // this part's steps
+  int part, parts, cell; // KV: part of the tile's steps; number of its (batch, KV head, tile)
   int ns, t_lo;          // else: as in the forward, key tiles of 64
   int dead_lo, dead_sk;
   // first moving row of step j, and (KV) its query head
@@ -87,16 +96,24 @@ template <bool KV> __device__ inline Item<KV> item_of(const WinBwdArgs& a, int i
   Item<KV> it{};
   if (KV) {
     // the tiles with sinks first: every later query sees them
-    const int heavy = a.heavy_tiles * g.B * g.Hk;
+    const int heavy = a.heavy_tiles * g.B * g.Hk * a.heavy_parts;
     int tile, bh;
     if (idx < heavy) {
+      it.parts = a.heavy_parts;
+      it.part = idx % it.parts;
+      idx /= it.parts;
       tile = idx % a.heavy_tiles;
       bh = idx / a.heavy_tiles;
     } else {
+      idx -= heavy;
+      it.parts = a.parts;
+      it.part = idx % it.parts;
+      idx /= it.parts;
       const int rest = a.tiles - a.heavy_tiles;
-      tile = a.heavy_tiles + (idx - heavy) % rest;
-      bh = (idx - heavy) / rest;
+      tile = a.heavy_tiles + idx % rest;
+      bh = idx / rest;
     }
+    it.cell = bh * a.tiles + tile;
     it.b = bh / g.Hk;
     it.hk = bh % g.Hk;
     it.row0 = 128 * tile;
@@ -118,6 +135,8 @@ template <bool KV> __device__ inline Item<KV> item_of(const WinBwdArgs& a, int i
         it.n = it.n_per * g.G;
       }
     }
+    it.j0 = (int)((long long)it.n * it.part / it.parts);
+    it.j1 = (int)((long long)it.n * (it.part + 1) / it.parts);
   } else {
     const int tile = a.tiles - 1 - idx % a.tiles;
     idx /= a.tiles;
@@ -144,6 +163,8 @@ template <bool KV> __device__ inline Item<KV> item_of(const WinBwdArgs& a, int i
     it.dead_lo = f.lo;
     const long long all_sk = (long long)g.sinks * g.unit;
     it.dead_sk = all_sk < f.lo ? (int)all_sk : f.lo;
+    it.parts = 1;
+    it.j1 = it.n;
   }
   return it;
 }
@@ -185,6 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->acc_empty, CTHREADS / 32);
+    mbar_init(&ctl->meet, CTHREADS / 32);
     mbar_init(&ctl->drain, 3);                   // final commit of each MMA warp
     ctl->abort = 0;
     fence_mbar_init();
@@ -212,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
       const Item<KV> it = item_of<KV>(a, idx);
-      if (it.n == 0) continue;
+      if (it.j0 == it.j1) continue;
       if (leader) {
         if (k >= 1) ok = mbar_wait(&ctl->stat_empty, (uint32_t)(k - 1) & 1, abort_flag, a.status, cap);
         if (ok) {
@@ -227,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       ++k;
-      for (int j = 0; j < it.n && ok; ++j, ++gs) {
+      for (int j = it.j0; j < it.j1 && ok; ++j, ++gs) {
         const int st = (int)(gs % MST);
         const int m0 = it.moving(j), hm = KV ? it.head(g, j) : it.hk;
         if (leader && gs >= MST)
@@ -276,7 +298,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t x = smem_u32(sStat) + (is_s ? 0u : C::STENSOR);
     const uint32_t tdst = tbase + (is_s ? Tm<KV>::S : Tm<KV>::DP);
     for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const int n = item_of<KV>(a, idx).n;
+      const Item<KV> it = item_of<KV>(a, idx);
+      const int n = it.j1 - it.j0;
       if (n == 0) continue;
       if (!mbar_wait_warp(&ctl->stat_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
       ++k;
@@ -313,10 +336,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
       const Item<KV> it = item_of<KV>(a, idx);
-      if (it.n == 0) continue;
+      if (it.j0 == it.j1) continue;
       if (k >= 1 && !mbar_wait_warp(&ctl->acc_empty, (uint32_t)(k - 1) & 1, abort_flag, a.status, cap)) break;
       ++k;
-      for (int j = 0; j < it.n; ++j, ++c) {
+      for (int j = it.j0; j < it.j1; ++j, ++c) {
         const int b = (int)(c % NB), st = (int)(c % MST);
         if (!mbar_wait_warp(&ctl->p_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap)) {
           ok = false;
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint64_t b0 = umma_desc_sw128(y0, MPART, 1024), b1 = umma_desc_sw128(y1, MPART, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t acc = (j == 0 && kk == 0) ? 0u : 1u;
+            const uint32_t acc = (j == it.j0 && kk == 0) ? 0u : 1u;
             const uint32_t col = 64 * b + 32 * (kk >> 1) + 8 * (kk & 1);
             if (KV)
               mma_ts(tbase + Tm<KV>::ACC1, tbase + Tm<KV>::S + col, b1 + ((kk * 2048) >> 4), C::IDESC_ACC, acc);  // dV
@@ -355,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           mma_commit(&ctl->mov_empty[st]);
           mma_commit(&ctl->step_done[b]);
-          if (j == it.n - 1) mma_commit(&ctl->acc_full);
+          if (j == it.j1 - 1) mma_commit(&ctl->acc_full);
         }
         __syncwarp();
       }
@@ -376,6 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float sl2 = g.scale * 1.4426950408889634f;
     long long c = 0;
     int k = 0;
+    uint32_t meets = 0;
     bool ok = true;
     for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
       const Item<KV> it = item_of<KV>(a, idx);
@@ -384,7 +408,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // moving rows this row meets: KV: queries [lo, hi); else keys [lo, hi) and [0, sk)
       Span sp{0, 0, 0};
       float lr = 0.f, dr = 0.f;
-      if (valid && it.n > 0) {
+      const bool steps = it.j0 < it.j1;
+      if (valid && steps) {
         if (KV) {
           const int off = it.seq.kvl - it.seq.ql, u = row / g.unit;
           sp.lo = u * g.unit - off;
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           dr = a.dd[at];
         }
       }
-      for (int j = 0; j < it.n; ++j, ++c) {
+      for (int j = it.j0; j < it.j1; ++j, ++c) {
         const int b = (int)(c % NB), st = (int)(c % MST);
         if (!mbar_wait(&ctl->s_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap)) {
           ok = false;
@@ -448,12 +473,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_arrive_warp(&ctl->p_full[b]);
       }
       if (!ok) break;
-      // ---- epilogue: accumulators to bf16 rows
-      if (it.n > 0) {
+      // ---- epilogue: accumulators to bf16 rows, or to this part's place in the workspace
+      if (steps) {
         if (!mbar_wait(&ctl->acc_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
         ++k;
         tc_fence_after();
       }
+      const bool whole = !KV || it.parts == 1;
 #pragma unroll 1
       for (int o = 0; o < (KV ? 2 : 1); ++o) {
         const uint32_t tacc = tbase + (o == 0 ? Tm<KV>::ACC0 : Tm<KV>::ACC1) + lane_off;
@@ -461,30 +487,87 @@ __global__ void __launch_bounds__(THREADS, 1)
         const WinOut& out = o == 0 ? a.out0 : a.out1;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.data) + (long long)it.b * out.batch +
                              (long long)(KV ? it.hk : it.h) * out.head + (long long)row * out.token;
+        float* pdst = whole ? nullptr : a.part + (((long long)idx * 2 + o) * 128 + r) * D;
 #pragma unroll 1
         for (int ch = part * (D / 64); ch < (part + 1) * (D / 64); ++ch) {
           uint32_t v[32];
-          if (it.n > 0) {
+          if (steps) {
             tmem_ld32(tacc + 32 * ch, v);
             tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if (valid) {
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = cvt_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
+          for (int i = 0; i < 32; ++i) v[i] = steps ? __float_as_uint(__uint_as_float(v[i]) * mul) : 0u;
+          if (!whole) {
+            uint4* d4 = reinterpret_cast<uint4*>(pdst + 32 * ch);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (valid) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * ch);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d4[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = cvt_bf16x2(__uint_as_float(v[8 * i + 2 * u]), __uint_as_float(v[8 * i + 2 * u + 1]));
+              d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
       }
-      if (it.n > 0) {
+      if (steps) {
         tc_fence_before();
         mbar_arrive_warp(&ctl->acc_empty);
+      }
+      if (!whole) {
+        // the last of the tile's parts to arrive adds them in ascending order
+        __threadfence();
+        mbar_arrive_warp(&ctl->meet);
+        if (!mbar_wait(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        if (threadIdx.x == CW0 * 32) ctl->last = atomicAdd(a.counters + it.cell, 1) == it.parts - 1;
+        mbar_arrive_warp(&ctl->meet);
+        if (!mbar_wait(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        if (ctl->last) {
+          __threadfence();
+          const float* src = a.part + (long long)(idx - it.part) * 2 * 128 * D;
+          const long long step = 2ll * 128 * D;
+          const int rows = it.seq.kvl - it.row0;             // rows past 128 or the sequence's end are not there
+          constexpr int NE = 4;                              // values asked for before one is used
+#pragma unroll 1
+          for (int e0 = threadIdx.x - CW0 * 32; e0 < 2 * 128 * D / 4; e0 += NE * CTHREADS) {
+            float acc[NE][4] = {};
+#pragma unroll 1
+            for (int p = 0; p < it.parts; p += 2) {
+              float4 v[2][NE];
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < NE; ++e)
+                  v[u][e] = p + u < it.parts
+                                ? __ldcg(reinterpret_cast<const float4*>(src + (p + u) * step) + e0 + e * CTHREADS)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                  acc[e][0] += v[u][e].x;
+                  acc[e][1] += v[u][e].y;
+                  acc[e][2] += v[u][e].z;
+                  acc[e][3] += v[u][e].w;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+              const int at = e0 + e * CTHREADS;
+              const int o = at / (32 * D), rr = at / (D / 4) % 128, d0 = at % (D / 4) * 4;
+              if (rr >= rows) continue;
+              const WinOut& out = o == 0 ? a.out0 : a.out1;
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.data) + (long long)it.b * out.batch +
+                                   (long long)it.hk * out.head + (long long)(it.row0 + rr) * out.token + d0;
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(cvt_bf16x2(acc[e][0], acc[e][1]), cvt_bf16x2(acc[e][2], acc[e][3]));
+            }
+          }
+        }
       }
     }
   }
