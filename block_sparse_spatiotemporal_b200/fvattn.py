@@ -447,40 +447,30 @@ def qkv_rope(shape: Shape, x, w, ws, bias=None, rope: Optional[Rope] = None, t_o
     return q, k, v
 
 
-class _Launch:
-    """Makes the tensors' device current and picks the stream to launch on
-    (the given one, or the device's current one; new outputs belong to it).
-    Does nothing more than read the stream when that is already so."""
-    __slots__ = ("dev", "stream", "guards")
-
-    def __init__(self, tensors, stream: Optional[torch.cuda.Stream]):
-        dev = -2
-        for t in tensors:
-            if t is None:
-                continue
+def _enter(tensors, stream: Optional[torch.cuda.Stream]):
+    """(stream handle, guards to close or None): makes the tensors' device
+    current and picks the stream to launch on, the given one or the device's
+    current one, which new outputs then belong to.  Where that is so already,
+    it only reads the stream."""
+    dev = -2
+    for t in tensors:
+        if t is not None:
             i = t.get_device()
-            if i < 0:
-                raise ValueError("expected a CUDA tensor")
             if i != dev:
+                if i < 0:
+                    raise ValueError("expected a CUDA tensor")
                 if dev != -2:
                     raise ValueError("expected every tensor on one device")
                 dev = i
-        if stream is not None and stream.device.index != dev:
-            raise ValueError("the stream belongs to another device than the tensors")
-        self.dev, self.stream, self.guards = dev, stream, None
-
-    def __enter__(self):
-        if self.stream is None and torch.cuda.current_device() == self.dev:
-            return torch.cuda.current_stream(self.dev).cuda_stream
-        self.guards = contextlib.ExitStack()
-        self.guards.enter_context(torch.cuda.device(self.dev))
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        self.guards.enter_context(torch.cuda.stream(s))
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guards is not None:
-            self.guards.close()
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return torch._C._cuda_getCurrentRawStream(dev), None
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    guards = contextlib.ExitStack()
+    guards.enter_context(torch.cuda.device(dev))
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    guards.enter_context(torch.cuda.stream(s))
+    return s.cuda_stream, guards
 
 
 def _typed(t: Optional[torch.Tensor], dtype, shape, what: str):
@@ -492,8 +482,7 @@ def _typed(t: Optional[torch.Tensor], dtype, shape, what: str):
     return t.data_ptr()
 
 
-def _torch_dtype(dtype: int):
-    return torch.bfloat16 if dtype == BF16 else torch.float32
+_DTYPES = {F32: torch.float32, BF16: torch.bfloat16}
 
 
 def make_norm(rows, channels, groups=1, dtype=BF16, eps=1e-6, gain_one=False, x_stride=0, y_stride=0) -> Norm:
@@ -509,28 +498,24 @@ def norm_workspace(norm: Norm, device="cuda") -> torch.Tensor:
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
-def _rows(t: Optional[torch.Tensor], norm: Norm, stride: int, what: str):
+def _rows(t: torch.Tensor, norm: Norm, stride: int, what: str):
     """Pointer of the rows of t: contiguous [..., channels], or [rows, channels] with norm's row stride."""
-    if t is None:
-        return None
-    stride = stride or norm.channels
-    ok = t.dtype == _torch_dtype(norm.dtype) and t.dim() >= 1 and t.shape[-1] == norm.channels and \
-        t.numel() == norm.rows * norm.channels
-    if ok and t.numel() > 0:
-        if t.is_contiguous():
-            ok = stride == norm.channels or norm.rows == 1
-        else:
-            ok = t.dim() == 2 and (t.stride(1) == 1 or norm.channels == 1) and (norm.rows == 1 or t.stride(0) == stride)
+    C, rows = norm.channels, norm.rows
+    stride = stride or C
+    ok = t.dtype is _DTYPES.get(norm.dtype) and t.dim() >= 1 and t.shape[-1] == C and t.numel() == rows * C
+    if ok and t.is_contiguous():
+        ok = stride == C or rows <= 1
+    elif ok:
+        ok = t.dim() == 2 and (t.stride(1) == 1 or C == 1) and (rows == 1 or t.stride(0) == stride)
     if not ok:
-        raise ValueError(f"{what}: expected {norm.rows} {_torch_dtype(norm.dtype)} rows of {norm.channels} "
-                         f"with row stride {stride}")
+        raise ValueError(f"{what}: expected {rows} {_DTYPES.get(norm.dtype)} rows of {C} with row stride {stride}")
     return t.data_ptr()
 
 
 def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
     """An output like `like` with norm's row stride."""
     if stride in (0, norm.channels) or norm.rows <= 1:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     buf = torch.empty(norm.rows * stride, dtype=like.dtype, device=like.device)
     return buf.as_strided((norm.rows, norm.channels), (stride, 1))
 
@@ -538,43 +523,54 @@ def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
 def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rstd=None, stream=None):
     """Layer norm of the rows of x ([..., channels]) with weight and bias
     [groups, channels] float32 (or None): returns (y, mean, rstd)."""
-    affine = (norm.groups, norm.channels)
-    with _Launch((x, weight, bias, y, mean, rstd), stream) as s:
+    affine, per_row = (norm.groups, norm.channels), (norm.rows,)
+    s, guards = _enter((x, weight, bias, y, mean, rstd), stream)
+    try:
         px = _rows(x, norm, norm.x_stride, "x")
         if y is None:
             y = _new_rows(x, norm, norm.y_stride)
-        if mean is None:
-            mean = torch.empty(norm.rows, dtype=torch.float32, device=x.device)
-        if rstd is None:
-            rstd = torch.empty(norm.rows, dtype=torch.float32, device=x.device)
+            py = y.data_ptr()
+        else:
+            py = _rows(y, norm, norm.y_stride, "y")
+        if mean is None and rstd is None:
+            mean, rstd = torch.empty((2, norm.rows), dtype=torch.float32, device=x.device).unbind(0)
+        elif mean is None:
+            mean = torch.empty_like(rstd)
+        elif rstd is None:
+            rstd = torch.empty_like(mean)
         _check("fvattn_layer_norm_fwd",
                lib().fvattn_layer_norm_fwd(ctypes.byref(norm), px, _typed(weight, torch.float32, affine, "weight"),
-                                           _typed(bias, torch.float32, affine, "bias"),
-                                           _rows(y, norm, norm.y_stride, "y"),
-                                           _typed(mean, torch.float32, (norm.rows,), "mean"),
-                                           _typed(rstd, torch.float32, (norm.rows,), "rstd"), s))
+                                           _typed(bias, torch.float32, affine, "bias"), py,
+                                           _typed(mean, torch.float32, per_row, "mean"),
+                                           _typed(rstd, torch.float32, per_row, "rstd"), s))
+    finally:
+        if guards is not None:
+            guards.close()
     return y, mean, rstd
 
 
 def layer_norm_bwd(norm: Norm, x, dy, mean, rstd, ws, weight=None, grads=None, stream=None):
     """Backward of layer_norm_fwd: returns (dx, dweight, dbias).  grads: the
     three output tensors, None for a gradient that is not wanted."""
-    affine = (norm.groups, norm.channels)
-    with _Launch((x, dy, mean, rstd, ws, weight, *(grads or ())), stream) as s:
+    affine, per_row = (norm.groups, norm.channels), (norm.rows,)
+    s, guards = _enter((x, dy, mean, rstd, ws, weight, *(grads or ())), stream)
+    try:
+        px = _rows(x, norm, norm.x_stride, "x")
         if grads is None:
             grads = (_new_rows(x, norm, norm.x_stride),
-                     torch.empty(affine, dtype=torch.float32, device=x.device),
-                     torch.empty(affine, dtype=torch.float32, device=x.device))
+                     *torch.empty((2, *affine), dtype=torch.float32, device=x.device).unbind(0))
         dx, dw, db = grads
         _check("fvattn_layer_norm_bwd",
-               lib().fvattn_layer_norm_bwd(ctypes.byref(norm), _rows(x, norm, norm.x_stride, "x"),
-                                           _rows(dy, norm, norm.y_stride, "dy"),
+               lib().fvattn_layer_norm_bwd(ctypes.byref(norm), px, _rows(dy, norm, norm.y_stride, "dy"),
                                            _typed(weight, torch.float32, affine, "weight"),
-                                           _typed(mean, torch.float32, (norm.rows,), "mean"),
-                                           _typed(rstd, torch.float32, (norm.rows,), "rstd"),
-                                           _rows(dx, norm, norm.x_stride, "dx"),
+                                           _typed(mean, torch.float32, per_row, "mean"),
+                                           _typed(rstd, torch.float32, per_row, "rstd"),
+                                           None if dx is None else _rows(dx, norm, norm.x_stride, "dx"),
                                            _typed(dw, torch.float32, affine, "dweight"),
                                            _typed(db, torch.float32, affine, "dbias"), _ptr(ws), ws.numel(), s))
+    finally:
+        if guards is not None:
+            guards.close()
     return dx, dw, db
 
 
@@ -610,7 +606,7 @@ def _new_heads(like: torch.Tensor, lens):
     """An output shaped and laid out like `like`; rows behind a sequence's
     length are not written by the library, so with lengths they start as 0."""
     if like.is_contiguous() or not like.transpose(1, 2).is_contiguous():
-        new = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        new = torch.empty_like(like, memory_format=torch.contiguous_format)
     else:                                               # token-major
         new = torch.empty_strided(like.shape, like.stride(), dtype=like.dtype, device=like.device)
     return new if lens is None else new.zero_()
@@ -621,7 +617,8 @@ def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, ls
     [B, kv_heads, kv_len, d] (any strides with contiguous rows): returns
     (out, lse).  q_lens, kv_lens: int32 device tensors [B] or None."""
     B, H, Hk, D = win.batch, win.heads, win.kv_heads, win.head_dim
-    with _Launch((q, k, v, ws, q_lens, kv_lens, out, lse), stream) as s:
+    s, guards = _enter((q, k, v, ws, q_lens, kv_lens, out, lse), stream)
+    try:
         vq = _view(q, B, H, win.q_len, D, "q")
         if out is None:
             out = _new_heads(q, q_lens)
@@ -635,6 +632,9 @@ def window_fwd(win: Window, q, k, v, ws, q_lens=None, kv_lens=None, out=None, ls
                                        _typed(kv_lens, torch.int32, (B,), "kv_lens"),
                                        _view(out, B, H, win.q_len, D, "out"),
                                        _typed(lse, torch.float32, (B, H, win.q_len), "lse"), _ptr(ws), ws.numel(), s))
+    finally:
+        if guards is not None:
+            guards.close()
     return out, lse
 
 
@@ -642,7 +642,8 @@ def window_bwd(win: Window, q, k, v, out, dout, lse, ws, q_lens=None, kv_lens=No
     """Backward of window_fwd (ws from ``window_workspace(win, backward=True)``):
     returns (dq, dk, dv).  grads: the three output tensors."""
     B, H, Hk, D = win.batch, win.heads, win.kv_heads, win.head_dim
-    with _Launch((q, k, v, out, dout, lse, ws, q_lens, kv_lens, *(grads or ())), stream) as s:
+    s, guards = _enter((q, k, v, out, dout, lse, ws, q_lens, kv_lens, *(grads or ())), stream)
+    try:
         vq, vk, vv = (_view(q, B, H, win.q_len, D, "q"), _view(k, B, Hk, win.kv_len, D, "k"),
                       _view(v, B, Hk, win.kv_len, D, "v"))
         if grads is None:
@@ -656,6 +657,9 @@ def window_bwd(win: Window, q, k, v, out, dout, lse, ws, q_lens=None, kv_lens=No
                                        _typed(kv_lens, torch.int32, (B,), "kv_lens"),
                                        _view(dq, B, H, win.q_len, D, "dq"), _view(dk, B, Hk, win.kv_len, D, "dk"),
                                        _view(dv, B, Hk, win.kv_len, D, "dv"), _ptr(ws), ws.numel(), s))
+    finally:
+        if guards is not None:
+            guards.close()
     return dq, dk, dv
 
 
