@@ -1334,6 +1334,10 @@ int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvat
   FV_TRY(make_query_map(&mq, *q, g, a.pack, a.tokens));
   FV_TRY(make_head_map(&mk, *k, g, g.Hk, g.Nk, 128, q->data));
   FV_TRY(make_head_map(&mv, *v, g, g.Hk, g.Nk, 128, q->data));
+  // the output's map serves the TMA stores; otherwise any map stands in its place
+  a.tma_out = a.dual && a.parts == 1 && a.pack == 1 && !q_lens;
+  CUtensorMap mo = mq;
+  if (a.tma_out) FV_TRY(make_head_map(&mo, *out, g, g.H, g.Nq, 32, q->data));
   a.out = out->data;
   a.o_batch = out->batch;
   a.o_head = out->head;
@@ -1348,7 +1352,7 @@ int fvattn_window_fwd(const fvattn_window* win, const fvattn_view* q, const fvat
   a.status = reinterpret_cast<int*>(base);
   a.wait_cap = kDefaultWaitCap;
   StageTimer t(FVATTN_STAGE_WINDOW, s);
-  FV_CUDA(launch_window_fwd(mq, mk, mv, a, dev.sms, s));
+  FV_CUDA(launch_window_fwd(mq, mk, mv, mo, a, dev.sms, s));
   t.kernels = 1;
   return FVATTN_OK;
 }

@@ -208,6 +208,7 @@ struct WinFwdArgs {
   int copies;                      // of the rows in a tile, each with its share of the keys (not dual): 1, 2 or 4
   int splits, parts;               // of an item's key tiles; parts written and joined (1: none)
   int n_items;
+  int tma_out;                     // output rows of a tile are consecutive and all there: stored by TMA
   void* out;
   long long o_batch, o_head, o_token;
   float* lse;                      // [B, H, Nq]
@@ -630,8 +631,8 @@ long long norm_bwd_blocks(long long rows);
 cudaError_t launch_norm_fwd(const NormArgs& a, int dtype, const void* x, void* y, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const void* x, const void* dy, void* dx, float* dw, float* db,
                             int num_sms, cudaStream_t s);
-cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
-                              int num_sms, cudaStream_t s);
+cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                              const WinFwdArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_window_prep(const WinGeom& g, const WinOut& out, const WinOut& dout, const float* lse, float* lse2,
                                float* dd, cudaStream_t s);
 cudaError_t launch_window_bwd(const CUtensorMap& s0, const CUtensorMap& s1, const CUtensorMap& m0,

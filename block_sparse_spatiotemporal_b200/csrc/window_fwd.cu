@@ -136,17 +136,17 @@ __device__ inline uint32_t chunk_mask(const Span& sp, int key0) {
   return bits(sp.lo - key0, sp.hi - key0) | bits(0, sp.sk - key0);
 }
 
-// P of a row's 64 logits, which start at tS, and their sum.
-template <bool MASKED>
-__device__ inline float exp_half(uint32_t tS, float sl2, float m, const Span& sp, int key0, uint32_t (&pk)[32]) {
+// P of a row's 64 logits (the first 32 in s0, the others in s1, on their way)
+// and their sum.  `next`: where the logits after them start; s0 leaves with
+// the first 32 of those on their way.
+template <bool MASKED, bool AHEAD>
+__device__ inline float exp_half(uint32_t (&s0)[32], uint32_t (&s1)[32], uint32_t next, float sl2, float m, const Span& sp,
+                                 int key0, uint32_t (&pk)[32]) {
   const uint64_t SL = f2(sl2, sl2), NM = f2(-m, -m);
   uint64_t acc[2] = {0ull, 0ull};
-  uint32_t s0[32], s1[32];
-  tmem_ld32(tS, s0);
-  tmem_wait_ld();
-  tmem_ld32(tS + 32, s1);
   exp_chunk<MASKED, false>(s0, SL, NM, MASKED ? chunk_mask(sp, key0) : 0u, pk, nullptr, acc);
   tmem_wait_ld();
+  if (AHEAD) tmem_ld32(next, s0);
   exp_chunk<MASKED, false>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32) : 0u, pk + 16, nullptr, acc);
   return sum2(add2(acc[0], acc[1]));
 }
@@ -237,6 +237,28 @@ template <bool DUAL> struct Turn {
     return DUAL ? key_tile < hi && (key_tile >= lo || key_tile < sk) : ((j - j0) & 1) == t;
   }
 };
+
+// The same to 32 consecutive rows of one head by a TMA store (the swizzle is
+// the map's), which runs on while the warp goes on; rows past the tensor's
+// end are not written.
+__device__ inline void store_rows_tma(uint8_t* stage, const uint32_t (&v)[32], const CUtensorMap* map, int dim, int row,
+                                      int head, int batch) {
+  const int lane = threadIdx.x & 31;
+  uint4* st = reinterpret_cast<uint4*>(stage);
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the store before is read
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st[lane * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+                 "r"(smem_u32(stage)), "r"(dim), "r"(row), "r"(head), "r"(batch)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
 
 // Writes 128 bytes of each of the warp's 32 rows (lane r: row r, 32 words in
 // v) to the rows' own addresses through the warp's staging: eight lanes write
@@ -358,7 +380,8 @@ struct JoinRows {
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                      const __grid_constant__ CUtensorMap mv, const WinFwdArgs a) {
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                      const WinFwdArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -405,8 +428,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tbase = ctl->tmem_base;
 
+  // Registers: the launch's 168 a thread (384 x 168) are 88 for these four
+  // warps and 208 for the softmax's eight, whose row of logits and
+  // probabilities spilled in 168.
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (lane == 0) {
       prefetch_tensormap(&mq);
       prefetch_tensormap(&mk);
@@ -464,6 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     long long seq = 0;               // ring number of the K tile of the item's first step
     int q_items = 0;                 // items with steps
     uint32_t cnt[2] = {0, 0};        // steps of each tile
@@ -482,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (j0 >= j1) continue;
       if (!mbar_wait_warp(&ctl->q_full, (uint32_t)q_items & 1, abort_flag, a.status, cap)) break;
       ++q_items;
-      bool first[2] = {true, true}, prev[2] = {false, false};
+      bool first[2] = {true, true}, prev[2] = {false, false}, done[2] = {false, false};
       int prev_key0 = 0;
       for (int j = j0; j <= j1 && ok; ++j) {
         const long long sk = seq + 2ll * (j - j0), sv = sk - 1;     // K of step j, V of step j - 1
@@ -510,6 +538,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = 0; t < 2; ++t) {
           const uint32_t tS = tb + TM_S + 128 * t, tO = tb + TM_O + 128 * t;
           if (prev[t]) {
+            // no step of this tile from here on: its key tiles ascend, sinks first
+            const bool last = DUAL ? j == j1 || kt >= turn[t].hi : j >= j1 - 1;
             if (first[t] && items[t] >= 1 &&
                 !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items[t] - 1) & 1, abort_flag, a.status, cap)) {
               ok = false;
@@ -531,13 +561,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                   if (!DUAL) mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
                 }
                 if (h == 0) mma_commit(&ctl->pv_half[t]);
-                if (h == 1 && j == j1) mma_commit(&ctl->o_full[t]);
+                if (h == 1 && last) mma_commit(&ctl->o_full[t]);
               }
               __syncwarp();
             }
             if (!ok) break;
             first[t] = false;
-          } else if (j == j1 && !first[t]) {     // its last PV was an earlier step's
+            done[t] = last;
+          } else if (j == j1 && !first[t] && !done[t]) {     // the rest of this split had no step for it
             if (elect_one()) mma_commit(&ctl->o_full[t]);
             __syncwarp();
           }
@@ -576,8 +607,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_drain(&ctl->drain, 0, a.status, cap);
     }
     __syncwarp();
-  } else if (warp >= SW0) {
+  } else if (warp < SW0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp - SW0) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -627,6 +661,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int key0 = 128 * kt;
           const bool masked = !(key0 + 128 <= hi_min && (key0 >= lo_max || key0 + 128 <= sk_min));
           if constexpr (DUAL) {
+            uint32_t s0[32], s1[32];
+            tmem_ld32(tS, s0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t tH = tS + 64 * h;
@@ -638,7 +674,12 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
               uint32_t pk[32];
               const float m_use = m == -INFINITY ? 0.f : m;
-              float sum = masked ? exp_half<true>(tH, sl2, m_use, sp, k0, pk) : exp_half<false>(tH, sl2, m_use, sp, k0, pk);
+              tmem_wait_ld();
+              tmem_ld32(tH + 32, s1);
+              float sum = h == 0 ? (masked ? exp_half<true, true>(s0, s1, tS + 64, sl2, m_use, sp, k0, pk)
+                                           : exp_half<false, true>(s0, s1, tS + 64, sl2, m_use, sp, k0, pk))
+                                 : (masked ? exp_half<true, false>(s0, s1, 0u, sl2, m_use, sp, k0, pk)
+                                           : exp_half<false, false>(s0, s1, 0u, sl2, m_use, sp, k0, pk));
               const bool over = valid && !(sum <= RESCALE_SUM);
               if (__any_sync(0xffffffffu, over)) {
                 // too large (or not a number): move the reference up and do
@@ -649,7 +690,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float m_new = over ? mx : m_use;
                 const float alpha = ex2(m_use - m_new);
                 if (over) m = m_new;
-                sum = exp_half<true>(tH, sl2, m_new, sp, k0, pk);
+                tmem_ld32(tH, s0);
+                tmem_wait_ld();
+                tmem_ld32(tH + 32, s1);
+                sum = exp_half<true, false>(s0, s1, 0u, sl2, m_new, sp, k0, pk);
+                if (h == 0) tmem_ld32(tS + 64, s0);
                 if (h == 1 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
                   ok = false;
                   break;
@@ -761,11 +806,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32(tO + ch * 64 + 32, o1);
             tmem_wait_ld();
           }
-          const bool none = !any || inv == 0.f;
+          // (a row that saw no key holds 0 where its tile had steps)
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            o0[x] = none ? 0u : __float_as_uint(__uint_as_float(o0[x]) * inv);
-            o1[x] = none ? 0u : __float_as_uint(__uint_as_float(o1[x]) * inv);
+            o0[x] = any ? __float_as_uint(__uint_as_float(o0[x]) * inv) : 0u;
+            o1[x] = any ? __float_as_uint(__uint_as_float(o1[x]) * inv) : 0u;
           }
           if (!DUAL) {
             if (valid) {
@@ -789,7 +834,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               tc_fence_before();
               mbar_arrive_warp(&ctl->o_empty[t]);
             }
-            store_rows(stage, w, row_ptr + ch * 128, valid);
+            if (a.tma_out)
+              store_rows_tma(stage, w, &mo, 64 * ch, tok0 + (warp & 3) * 32, head0, batch);
+            else
+              store_rows(stage, w, row_ptr + ch * 128, valid);
           }
         }
         if (valid) {
@@ -850,6 +898,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
+    if (DUAL && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // shared memory is read
   }
 
   __syncthreads();
@@ -860,25 +909,25 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int D, bool DUAL>
-cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
-                       int num_sms, cudaStream_t s) {
+cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                       const WinFwdArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int grid = a.n_items < num_sms ? a.n_items : num_sms;
-  window_fwd_kernel<D, DUAL><<<grid, THREADS, Cfg<D>::SMEM, s>>>(mq, mk, mv, a);
+  window_fwd_kernel<D, DUAL><<<grid, THREADS, Cfg<D>::SMEM, s>>>(mq, mk, mv, mo, a);
   return cudaGetLastError();
 }
 
 }  // namespace win
 
-cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const WinFwdArgs& a,
-                              int num_sms, cudaStream_t s) {
+cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                              const WinFwdArgs& a, int num_sms, cudaStream_t s) {
   if (a.g.D == 128)
-    return a.dual ? win::launch_fwd<128, true>(mq, mk, mv, a, num_sms, s)
-                  : win::launch_fwd<128, false>(mq, mk, mv, a, num_sms, s);
-  return a.dual ? win::launch_fwd<64, true>(mq, mk, mv, a, num_sms, s)
-                : win::launch_fwd<64, false>(mq, mk, mv, a, num_sms, s);
+    return a.dual ? win::launch_fwd<128, true>(mq, mk, mv, mo, a, num_sms, s)
+                  : win::launch_fwd<128, false>(mq, mk, mv, mo, a, num_sms, s);
+  return a.dual ? win::launch_fwd<64, true>(mq, mk, mv, mo, a, num_sms, s)
+                : win::launch_fwd<64, false>(mq, mk, mv, mo, a, num_sms, s);
 }
 
 }  // namespace fvattn
