@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
   unsigned char* base = ring_smem + L.id * 2 * STAGES * Rg::bytes(L.team);
   const Rg rx{base, pl, team, t, a.C}, ry{base + STAGES * Rg::bytes(L.team), pl, team, t, a.C};
   const Ch ch{pl};
-  // sums over the teams: [EPT][team]
+  // sums of the teams: [teams][C]
   float* sw = reinterpret_cast<float*>(ring_smem + ring_end(L.teams * 2 * STAGES * Rg::bytes(L.team)));
   const float inv_c = 1.f / (float)a.C;
   const Range rg = block_rows(a);
@@ -512,25 +512,28 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
       float* out = a.partial + ((long long)blockIdx.x + g) * 2 * a.C;
 #pragma unroll
       for (int h = 0; h < 2; ++h, out += a.C) {
-        for (int id = 0; id < L.teams; ++id) {    // over the teams, in order
-          if (L.id == id) {
+        if (L.teams > 1 && (h == 1 || s0 > rg.r0)) __syncthreads();      // the sums before are read
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-              float f[CE];
+        for (int k = 0; k < N; ++k) {
+          float f[CE];
 #pragma unroll
-              for (int i = 0; i < NP; ++i) uf2(h ? ab[k * NP + i] : aw[k * NP + i], f[2 * i], f[2 * i + 1]);
+          for (int i = 0; i < NP; ++i) uf2(h ? ab[k * NP + i] : aw[k * NP + i], f[2 * i], f[2 * i + 1]);
 #pragma unroll
-              for (int i = 0; i < CE; ++i) {
-                float* c = sw + (k * CE + i) * team + t;
-                if (id > 0) f[i] += *c;
-                if (id < L.teams - 1)
-                  *c = f[i];
-                else if (ch.on(k, i))
-                  out[ch.col(k, i)] = f[i];
-              }
+          for (int i = 0; i < CE; ++i)
+            if (ch.on(k, i)) {
+              if (L.teams > 1)
+                sw[L.id * a.C + ch.col(k, i)] = f[i];
+              else
+                out[ch.col(k, i)] = f[i];
             }
+        }
+        if (L.teams > 1) {           // over the teams, in order
+          __syncthreads();
+          for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
+            float v = sw[c];
+            for (int id = 1; id < L.teams; ++id) v += sw[id * a.C + c];
+            out[c] = v;
           }
-          if (L.teams > 1) __syncthreads();
         }
       }
     }
@@ -739,7 +742,7 @@ cudaError_t bwd_v(NormArgs a, const T* x, const T* dy, T* dx, cudaStream_t s) {
   auto kernel = a.C == 32 * EPT * a.warps ? norm_bwd_kernel<T, VEC, EPT, true> : norm_bwd_kernel<T, VEC, EPT, false>;
   // as many teams as the warps allow, as many as the shared memory takes, one block an SM
   int teams = WARPS / a.warps < MAX_TEAMS ? WARPS / a.warps : MAX_TEAMS;
-  auto bytes = [&](int n) { return ring_end(n * 2 * Rg::STAGES * Rg::bytes(32 * a.warps)) + (n > 1 ? 4 * EPT * 32 * a.warps : 0); };
+  auto bytes = [&](int n) { return ring_end(n * 2 * Rg::STAGES * Rg::bytes(32 * a.warps)) + (n > 1 ? 4 * a.C * n : 0); };
   while (teams > 1 && bytes(teams) > 220 * 1024) --teams;
   const int smem = bytes(teams);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -34,7 +34,7 @@ struct Span {
 __device__ inline Span span_of(const WinGeom& g, const Seq& s, int i) {
   const int p = i + s.kvl - s.ql;
   if (p < 0) return {0, 0, 0};
-  const int u = p / g.unit;
+  const int u = g.unit == 1 ? p : p / g.unit;
   const long long end = ((long long)u + 1) * g.unit;
   const int hi = end < s.kvl ? (int)end : s.kvl;
   const int u0 = g.window > 0 && u >= g.window ? u - g.window + 1 : 0;
