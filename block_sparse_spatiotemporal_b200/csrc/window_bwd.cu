@@ -68,8 +68,8 @@ struct Ctl {
   uint64_t acc_empty;        // the epilogue read them (8 warps)
   uint64_t meet;             // the compute warps meet (8 warps)
   uint64_t drain;
-  float lse2[MAXST][64];     // key-stationary only: lse * log2(e) of the step's queries
-  float dd[MAXST][64];       //   and their rowsum(dout * out)
+  alignas(16) float lse2[MAXST][64];     // key-stationary only: lse * log2(e) of the step's queries
+  alignas(16) float dd[MAXST][64];       //   and their rowsum(dout * out)
   uint32_t tmem_base;
   int abort;
   int last;                  // this part was its tile's last
@@ -442,19 +442,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld32(tS, s);
         tmem_ld32(tD, dp);
         tmem_wait_ld();
+        const uint64_t SL = both(sl2);
+        const float4* l4 = reinterpret_cast<const float4*>(&ctl->lse2[st][32 * part]);
+        const float4* d4 = reinterpret_cast<const float4*>(&ctl->dd[st][32 * part]);
+        float x[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float p[2], d[2];
+        for (int i = 0; i < 8; ++i) {              // four columns at a time: p = 2^(s' - lse2)
+          uint64_t n0, n1;
+          if (KV) {
+            const float4 l = l4[i];
+            n0 = f2(-l.x, -l.y);
+            n1 = f2(-l.z, -l.w);
+          } else {
+            n0 = n1 = both(-lr);
+          }
+          uf2(fma2(f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), SL, n0), x[4 * i], x[4 * i + 1]);
+          uf2(fma2(f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), SL, n1), x[4 * i + 2], x[4 * i + 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = ex2(x[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {              // ds = p (dp - dd)
+          uint64_t n0, n1;
+          if (KV) {
+            const float4 d = d4[i];
+            n0 = f2(d.x, d.y);
+            n1 = f2(d.z, d.w);
+          } else {
+            n0 = n1 = both(dr);
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int col = 2 * i + u;
-            const float l2 = KV ? ctl->lse2[st][32 * part + col] : lr;
-            const float dv = KV ? ctl->dd[st][32 * part + col] : dr;
-            p[u] = ex2(fmaf(__uint_as_float(s[col]), sl2, -l2));
-            d[u] = p[u] * (__uint_as_float(dp[col]) - dv);
+            const int c2 = 4 * i + 2 * u;
+            float a0, a1;
+            uf2(mul2(f2(x[c2], x[c2 + 1]),
+                     sub2(f2(__uint_as_float(dp[c2]), __uint_as_float(dp[c2 + 1])), u ? n1 : n0)), a0, a1);
+            pk[2 * i + u] = cvt_bf16x2(x[c2], x[c2 + 1]);
+            dk[2 * i + u] = cvt_bf16x2(a0, a1);
           }
-          pk[i] = cvt_bf16x2(p[0], p[1]);
-          dk[i] = cvt_bf16x2(d[0], d[1]);
         }
         if (masked) {
 #pragma unroll
