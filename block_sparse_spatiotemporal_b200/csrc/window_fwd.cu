@@ -17,9 +17,11 @@
 //                3,000 clocks on its divisions), loads its Q and its K and V
 //                tiles, these through one ring;
 //   warp 1       MMAs, for tile A and then tile B of every step:
-//                O_g += P_g(j-1) V in two halves of 64 keys as the softmax
-//                hands them over, then S_g(j) = Q_g K^T into the TMEM columns
-//                P_g(j-1) held (MMAs of one thread run in issue order).  The
+//                O_g += P_g(j-1) V, then S_g(j) = Q_g K^T into the TMEM
+//                columns P_g(j-1) held (MMAs of one thread run in issue
+//                order; handing P over in halves of 64 keys, for an earlier
+//                start, cost more in fences than it won: 227 against 211 us
+//                at 2 x 32 heads, 4,099 tokens, window 1,024).  The
 //                fixed order keeps the tiles half a step apart, so that one's
 //                products run during the other's softmax; with a warp of its
 //                own for each tile both fell into step, exponentials against
@@ -45,9 +47,9 @@
 // arrive (a counter per item) joins the parts in ascending order, so the
 // result does not depend on which that is.
 //
-// TMEM (512 columns): S_A, S_B at 0, 128, O_A, O_B at 256, 384.  P goes over S:
-// each 64 keys' over the first 32 of their columns, or, with its second bf16,
-// each 32 keys' two halves over their own columns.  Shared memory: Q 2 x
+// TMEM (512 columns): S_A, S_B at 0, 128, O_A, O_B at 256, 384.  P goes over
+// the first 64 columns of S, or, with its second bf16, each 32 keys' two parts
+// over their own columns.  Shared memory: Q 2 x
 // 128 rows, ring of 128-key tiles, all in 128-byte swizzled parts of 64 dims;
 // 4 KB a softmax warp for the output.
 #include "window.cuh"
@@ -92,8 +94,7 @@ struct FwdCtl {
   uint64_t q_full, q_empty;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2];      // S_g of its next step written (and every earlier MMA of the tile complete)
-  uint64_t p_full[2][2];   // half h of P_g written (4 warps)
-  uint64_t pv_half[2];     // PV of the first half of P_g complete
+  uint64_t p_full[2];      // P_g written (4 warps)
   uint64_t o_full[2];      // the item's last PV of tile g complete
   uint64_t o_empty[2];     // O_g read (4 warps)
   uint64_t group[2];       // softmax group t meets (4 warps)
@@ -136,18 +137,25 @@ __device__ inline uint32_t chunk_mask(const Span& sp, int key0) {
   return bits(sp.lo - key0, sp.hi - key0) | bits(0, sp.sk - key0);
 }
 
-// P of a row's 64 logits (the first 32 in s0, the others in s1, on their way)
-// and their sum.  `next`: where the logits after them start; s0 leaves with
-// the first 32 of those on their way.
-template <bool MASKED, bool AHEAD>
-__device__ inline float exp_half(uint32_t (&s0)[32], uint32_t (&s1)[32], uint32_t next, float sl2, float m, const Span& sp,
-                                 int key0, uint32_t (&pk)[32]) {
+// P of a row's 128 logits, which start at tS, and their sum.  32 logits are on
+// their way while 32 are worked on.
+template <bool MASKED>
+__device__ inline float exp_row(uint32_t tS, float sl2, float m, const Span& sp, int key0, uint32_t (&pk)[64]) {
   const uint64_t SL = f2(sl2, sl2), NM = f2(-m, -m);
   uint64_t acc[2] = {0ull, 0ull};
+  uint32_t s0[32], s1[32];
+  tmem_ld32(tS, s0);
+  tmem_wait_ld();
+  tmem_ld32(tS + 32, s1);
   exp_chunk<MASKED, false>(s0, SL, NM, MASKED ? chunk_mask(sp, key0) : 0u, pk, nullptr, acc);
   tmem_wait_ld();
-  if (AHEAD) tmem_ld32(next, s0);
+  tmem_ld32(tS + 64, s0);
   exp_chunk<MASKED, false>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 32) : 0u, pk + 16, nullptr, acc);
+  tmem_wait_ld();
+  tmem_ld32(tS + 96, s1);
+  exp_chunk<MASKED, false>(s0, SL, NM, MASKED ? chunk_mask(sp, key0 + 64) : 0u, pk + 32, nullptr, acc);
+  tmem_wait_ld();
+  exp_chunk<MASKED, false>(s1, SL, NM, MASKED ? chunk_mask(sp, key0 + 96) : 0u, pk + 48, nullptr, acc);
   return sum2(add2(acc[0], acc[1]));
 }
 
@@ -161,6 +169,14 @@ __device__ inline float max_chunk(uint32_t tS, const Span& sp, int key0) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     if ((mask >> i) & 1u) m = fmaxf(m, __uint_as_float(s[i]));
+  return m;
+}
+
+// The same of all 128.
+__device__ inline float max_row(uint32_t tS, const Span& sp, int key0) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) m = fmaxf(m, max_chunk(tS + 32 * c, sp, key0 + 32 * c));
   return m;
 }
 
@@ -408,9 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i][0], 4);
-      mbar_init(&ctl->p_full[i][1], 4);
-      mbar_init(&ctl->pv_half[i], 1);
+      mbar_init(&ctl->p_full[i], 4);
       mbar_init(&ctl->o_full[i], 1);
       mbar_init(&ctl->o_empty[i], 4);
       mbar_init(&ctl->group[i], 4);
@@ -545,27 +559,22 @@ __global__ void __launch_bounds__(THREADS, 1)
               ok = false;
               break;
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait_warp(&ctl->p_full[t][h], (cnt[t] - 1) & 1, abort_flag, a.status, cap)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-                const uint64_t vd = umma_desc_sw128(v_at, PART, 1024);
-#pragma unroll
-                for (int kk = 4 * h; kk < 4 * h + 4; ++kk) {
-                  const uint32_t tP = DUAL ? tS + 64 * h + 8 * (kk - 4 * h) : tS + 32 * (kk >> 1) + 8 * (kk & 1);
-                  mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
-                  if (!DUAL) mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
-                }
-                if (h == 0) mma_commit(&ctl->pv_half[t]);
-                if (h == 1 && last) mma_commit(&ctl->o_full[t]);
-              }
-              __syncwarp();
+            if (!mbar_wait_warp(&ctl->p_full[t], (cnt[t] - 1) & 1, abort_flag, a.status, cap)) {
+              ok = false;
+              break;
             }
-            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = umma_desc_sw128(v_at, PART, 1024);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t tP = DUAL ? tS + 8 * kk : tS + 32 * (kk >> 1) + 8 * (kk & 1);
+                mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
+                if (!DUAL) mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
+              }
+              if (last) mma_commit(&ctl->o_full[t]);
+            }
+            __syncwarp();
             first[t] = false;
             done[t] = last;
           } else if (j == j1 && !first[t] && !done[t]) {     // the rest of this split had no step for it
@@ -661,54 +670,31 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int key0 = 128 * kt;
           const bool masked = !(key0 + 128 <= hi_min && (key0 >= lo_max || key0 + 128 <= sk_min));
           if constexpr (DUAL) {
-            uint32_t s0[32], s1[32];
-            tmem_ld32(tS, s0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t tH = tS + 64 * h;
-              const int k0 = key0 + 64 * h;
-              if (unset) {                       // some row has met no visible key yet
-                const float mx = fmaxf(max_chunk(tH, sp, k0), max_chunk(tH + 32, sp, k0 + 32)) * sl2;
-                if (m == -INFINITY) m = mx;
-                unset = __any_sync(0xffffffffu, m == -INFINITY);
-              }
-              uint32_t pk[32];
-              const float m_use = m == -INFINITY ? 0.f : m;
-              tmem_wait_ld();
-              tmem_ld32(tH + 32, s1);
-              float sum = h == 0 ? (masked ? exp_half<true, true>(s0, s1, tS + 64, sl2, m_use, sp, k0, pk)
-                                           : exp_half<false, true>(s0, s1, tS + 64, sl2, m_use, sp, k0, pk))
-                                 : (masked ? exp_half<true, false>(s0, s1, 0u, sl2, m_use, sp, k0, pk)
-                                           : exp_half<false, false>(s0, s1, 0u, sl2, m_use, sp, k0, pk));
-              const bool over = valid && !(sum <= RESCALE_SUM);
-              if (__any_sync(0xffffffffu, over)) {
-                // too large (or not a number): move the reference up and do
-                // the half again.  Before the first half every earlier MMA of
-                // the tile is complete (so says S); before the second, the
-                // first half's PV has to be.
-                const float mx = fmaxf(fmaxf(max_chunk(tH, sp, k0), max_chunk(tH + 32, sp, k0 + 32)) * sl2, m_use);
-                const float m_new = over ? mx : m_use;
-                const float alpha = ex2(m_use - m_new);
-                if (over) m = m_new;
-                tmem_ld32(tH, s0);
-                tmem_wait_ld();
-                tmem_ld32(tH + 32, s1);
-                sum = exp_half<true, false>(s0, s1, 0u, sl2, m_new, sp, k0, pk);
-                if (h == 0) tmem_ld32(tS + 64, s0);
-                if (h == 1 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                scale_o<D>(tO, alpha);           // before an item's first PV it holds nothing that is used
-                l *= alpha;
-              }
-              l += sum;
-              tmem_st32(tH, pk);
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive_warp(&ctl->p_full[t][h]);
+            if (unset) {                         // some row has met no visible key yet
+              const float mx = max_row(tS, sp, key0) * sl2;
+              if (m == -INFINITY) m = mx;
+              unset = __any_sync(0xffffffffu, m == -INFINITY);
             }
+            uint32_t pk[64];
+            const float m_use = m == -INFINITY ? 0.f : m;
+            float sum = masked ? exp_row<true>(tS, sl2, m_use, sp, key0, pk) : exp_row<false>(tS, sl2, m_use, sp, key0, pk);
+            const bool over = valid && !(sum <= RESCALE_SUM);
+            if (__any_sync(0xffffffffu, over)) {
+              // too large (or not a number): move the reference up and do the
+              // row again.  Every earlier MMA of the tile is complete (so says
+              // S), so O holds the earlier steps; before an item's first PV it
+              // holds nothing that is used.
+              const float mx = fmaxf(max_row(tS, sp, key0) * sl2, m_use);
+              const float m_new = over ? mx : m_use;
+              const float alpha = ex2(m_use - m_new);
+              if (over) m = m_new;
+              sum = exp_row<true>(tS, sl2, m_new, sp, key0, pk);
+              scale_o<D>(tO, alpha);
+              l *= alpha;
+            }
+            l += sum;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st16(tS + 16 * c, pk + 16 * c);
           } else {
             // 32 keys at a time, P as two bf16 in the columns of their logits
 #pragma unroll 1
@@ -735,20 +721,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                   sum = sum2(add2(acc[0], acc[1]));
                   const bool over = again == 0 && valid && !(sum <= RESCALE_SUM);
                   if (!__any_sync(0xffffffffu, over)) break;
-                  // as above; what this half already holds of P moves too
+                  // as above; what this step already holds of P moves too
                   const float m_new = over ? fmaxf(max_chunk(tC, sp, k0) * sl2, m_use) : m_use;
                   const float alpha = ex2(m_use - m_new);
                   if (over) m = m_new;
                   m_use = m_new;
-                  if (c >= 2 && !mbar_wait(&ctl->pv_half[t], cnt & 1, abort_flag, a.status, cap)) {
-                    ok = false;
-                    break;
-                  }
-                  tc_fence_after();
                   scale_o<D>(tO, alpha);
                   l *= alpha;
-                  if ((c & 1) && ((chunks >> (c - 1)) & 1u)) {
-                    tmem_ld32(tC - 32, s);
+#pragma unroll 1
+                  for (int e = 0; e < c; ++e) {
+                    if (!((chunks >> e) & 1u)) continue;
+                    tmem_ld32(tS + 32 * e, s);
                     tmem_wait_ld();
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
@@ -757,29 +740,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                       s[x] = cvt_bf16x2(p0, p1);
                       s[16 + x] = cvt_bf16x2(p0 - __uint_as_float(s[x] << 16), p1 - __uint_as_float(s[x] & 0xFFFF0000u));
                     }
-                    tmem_st32(tC - 32, s);
+                    tmem_st32(tS + 32 * e, s);
                   }
                 }
-                if (!ok) break;
                 l += sum;
               } else {
 #pragma unroll
                 for (int x = 0; x < 32; ++x) pk[x] = 0u;
               }
               tmem_st32(tC, pk);
-              if (c & 1) {
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive_warp(&ctl->p_full[t][c >> 1]);
-              }
             }
           }
-          if (!ok) break;
-        } else {
-          tc_fence_before();
-          mbar_arrive_warp(&ctl->p_full[t][0]);
-          mbar_arrive_warp(&ctl->p_full[t][1]);
+          tmem_wait_st();
         }
+        tc_fence_before();
+        mbar_arrive_warp(&ctl->p_full[t]);
         ++cnt;
       }
       if (!ok) break;
