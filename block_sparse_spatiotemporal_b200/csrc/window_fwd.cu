@@ -66,14 +66,17 @@ constexpr uint32_t TMEM_COLS = 512, TM_S = 0, TM_O = 256;
 constexpr int ITEMS = 2;                     // items published ahead
 constexpr uint32_t OUT_STAGE = 32 * 128;     // 32 rows x 128 bytes a softmax warp
 
-template <int D> struct Cfg {
-  static constexpr int PARTS = D / 64;
+// The single form holds one query tile, which leaves the ring a stage more:
+// what is on its way from memory is what bounds it.
+template <int D, bool DUAL> struct Cfg {
+  static constexpr int PARTS = D / 64, QTILES = DUAL ? 2 : 1;
   static constexpr uint32_t TILE = PART * PARTS;        // 128 rows
-  static constexpr int NST = D == 128 ? 4 : 8;          // ring of K and V tiles
-  static constexpr uint32_t SMEM = 1024 + 2 * TILE + NST * TILE + 8 * OUT_STAGE;
+  static constexpr int NST = (D == 128 ? 6 : 12) - QTILES * (D == 128 ? 1 : 2);   // ring of K and V tiles
+  static constexpr uint32_t SMEM = 1024 + QTILES * TILE + NST * TILE + 8 * OUT_STAGE;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
 };
+constexpr int MAXST = 10;
 
 // Item and its key tiles.
 struct Item {
@@ -90,11 +93,12 @@ struct Item {
 };
 
 struct FwdCtl {
-  uint64_t item_full[ITEMS], item_empty[ITEMS];   // the MMA warp and 8 softmax warps read an item
+  uint64_t item_full[ITEMS], item_empty[ITEMS];   // the MMA warps and 8 softmax warps read an item
   uint64_t q_full, q_empty;
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t kv_full[MAXST], kv_empty[MAXST];
   uint64_t s_full[2];      // S_g of its next step written (and every earlier MMA of the tile complete)
   uint64_t p_full[2];      // P_g written (4 warps)
+  uint64_t pv_done[2];     // single form: the PV of a step of group g complete
   uint64_t o_full[2];      // the item's last PV of tile g complete
   uint64_t o_empty[2];     // O_g read (4 warps)
   uint64_t group[2];       // softmax group t meets (4 warps)
@@ -104,7 +108,10 @@ struct FwdCtl {
   int last[2];             // this group's part was the item's last
   Item item[ITEMS];
 };
-static_assert(Cfg<128>::SMEM + sizeof(FwdCtl) <= 232448 && Cfg<64>::SMEM + sizeof(FwdCtl) <= 232448, "shared memory");
+static_assert(Cfg<128, true>::SMEM + sizeof(FwdCtl) <= 232448 && Cfg<128, false>::SMEM + sizeof(FwdCtl) <= 232448 &&
+                  Cfg<64, true>::SMEM + sizeof(FwdCtl) <= 232448 && Cfg<64, false>::SMEM + sizeof(FwdCtl) <= 232448 &&
+                  Cfg<64, false>::NST <= MAXST,
+              "shared memory");
 
 // P of 32 logits as 16 bf16x2 words (and what they round away as 16 more),
 // their fp32 sum added to acc.  In three sweeps: one pair after another waits
@@ -398,11 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
                       const WinFwdArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, DUAL>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * C::TILE;
+  uint8_t* sKV = smem + C::QTILES * C::TILE;
   uint8_t* sOut = sKV + C::NST * C::TILE;
   __shared__ FwdCtl ctl_s;
   FwdCtl* ctl = &ctl_s;
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], 9);
+      mbar_init(&ctl->item_empty[i], DUAL ? 9 : 10);
     }
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->q_empty, 1);
@@ -425,11 +432,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->pv_done[i], 1);
       mbar_init(&ctl->o_full[i], 1);
       mbar_init(&ctl->o_empty[i], 4);
       mbar_init(&ctl->group[i], 4);
     }
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain, DUAL ? 1 : 2);         // a final commit of each MMA warp
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -503,8 +511,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(&ctl->kv_full[i], (uint32_t)(last / C::NST) & 1, a.status, cap);
       }
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMAs
+  } else if (DUAL && warp == 1) {
+    // ------------------------------------------------------ MMAs, two tiles
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     long long seq = 0;               // ring number of the K tile of the item's first step
     int q_items = 0;                 // items with steps
@@ -531,6 +539,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int stk = (int)(sk % C::NST), stv = (int)(sv % C::NST);
         const uint32_t k_at = uni(kv_base + stk * C::TILE), v_at = uni(kv_base + stv * C::TILE);
         const int kt = j < ns ? j : t_lo + j - ns;
+        auto issue_s = [&](int t) {
+          if (elect_one()) {
+            const uint64_t qd = umma_desc_sw128(q_at + t * C::TILE, 16, 1024);
+            const uint64_t kd = umma_desc_sw128(k_at, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * PART + (kk & 3) * 32) >> 4;
+              mma_ss(tb + TM_S + 128 * t, qd + off, kd + off, C::IDESC_S, kk ? 1u : 0u);
+            }
+            mma_commit(&ctl->s_full[t]);
+          }
+          __syncwarp();
+          ++cnt[t];
+        };
         if (j > j0) {
           if (!mbar_wait_warp(&ctl->kv_full[stv], (uint32_t)(sv / C::NST) & 1, abort_flag, a.status, cap)) {
             ok = false;
@@ -553,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t tS = tb + TM_S + 128 * t, tO = tb + TM_O + 128 * t;
           if (prev[t]) {
             // no step of this tile from here on: its key tiles ascend, sinks first
-            const bool last = DUAL ? j == j1 || kt >= turn[t].hi : j >= j1 - 1;
+            const bool last = j == j1 || kt >= turn[t].hi;
             if (first[t] && items[t] >= 1 &&
                 !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items[t] - 1) & 1, abort_flag, a.status, cap)) {
               ok = false;
@@ -568,9 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               const uint64_t vd = umma_desc_sw128(v_at, PART, 1024);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t tP = DUAL ? tS + 8 * kk : tS + 32 * (kk >> 1) + 8 * (kk & 1);
-                mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
-                if (!DUAL) mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
+                mma_ts(tO, tS + 8 * kk, vd + ((kk * 2048) >> 4), C::IDESC_PV, first[t] && kk == 0 ? 0u : 1u);
               }
               if (last) mma_commit(&ctl->o_full[t]);
             }
@@ -582,20 +602,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
           }
           prev[t] = j < j1 && turn[t].on(j, kt);
-          if (prev[t]) {
-            if (elect_one()) {
-              const uint64_t qd = umma_desc_sw128(q_at + (DUAL ? t : 0) * C::TILE, 16, 1024);
-              const uint64_t kd = umma_desc_sw128(k_at, 16, 1024);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * PART + (kk & 3) * 32) >> 4;
-                mma_ss(tS, qd + off, kd + off, C::IDESC_S, kk ? 1u : 0u);
-              }
-              mma_commit(&ctl->s_full[t]);
-            }
-            __syncwarp();
-            ++cnt[t];
-          }
+          if (prev[t]) issue_s(t);
         }
         if (!ok) break;
         if (elect_one()) {
@@ -611,6 +618,95 @@ __global__ void __launch_bounds__(THREADS, 1)
       seq += 2ll * (j1 - j0);
     }
     // every MMA issued has completed before TMEM is freed
+    if (elect_one()) {
+      mma_commit(&ctl->drain);
+      mbar_drain(&ctl->drain, 0, a.status, cap);
+    }
+    __syncwarp();
+  } else if (!DUAL && (warp == 1 || warp == 2)) {
+    // ------------------------------------------------- MMAs, single form
+    // Warp 1 issues the S of every step as its K arrives, warp 2 the PV as its
+    // P is written: bound by memory, neither waits for what the other needs.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const bool is_s = warp == 1;
+    long long seq = 0;               // ring number of the K tile of the item's first step
+    int q_items = 0;
+    uint32_t cnt[2] = {0, 0};        // steps of each group
+    int items[2] = {0, 0};           // items whose O_t was written
+    bool ok = true;
+    const uint32_t q_at = uni(smem_u32(sQ)), kv_base = smem_u32(sKV), tb = uni(tbase);
+    for (int n = 0; ok; ++n) {
+      const int ib = n % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item& si = ctl->item[ib];
+      const int idx = si.idx, j0 = si.j0, j1 = si.j1, ns = si.ns, t_lo = si.t_lo, kvl = si.seq.kvl;
+      const int dead_lo = si.dead_lo, dead_sk = si.dead_sk;
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      if (idx < 0) break;
+      if (j0 >= j1) continue;
+      if (is_s && !mbar_wait_warp(&ctl->q_full, (uint32_t)q_items & 1, abort_flag, a.status, cap)) break;
+      ++q_items;
+      for (int j = j0; j < j1; ++j) {
+        const int t = (j - j0) & 1;
+        const long long at = seq + 2ll * (j - j0) + (is_s ? 0 : 1);
+        const int st = (int)(at % C::NST);
+        const uint32_t tile_at = uni(kv_base + st * C::TILE), tS = uni(tb + TM_S + 128 * t), tO = uni(tb + TM_O + 128 * t);
+        if (!mbar_wait_warp(&ctl->kv_full[st], (uint32_t)(at / C::NST) & 1, abort_flag, a.status, cap)) {
+          ok = false;
+          break;
+        }
+        if (is_s) {
+          // the group's last P, in the columns of this S, is read
+          if (cnt[t] >= 1 && !mbar_wait_warp(&ctl->pv_done[t], (cnt[t] - 1) & 1, abort_flag, a.status, cap)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t qd = umma_desc_sw128(q_at, 16, 1024), kd = umma_desc_sw128(tile_at, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * PART + (kk & 3) * 32) >> 4;
+              mma_ss(tS, qd + off, kd + off, C::IDESC_S, kk ? 1u : 0u);
+            }
+            mma_commit(&ctl->s_full[t]);
+            mma_commit(&ctl->kv_empty[st]);
+            if (j == j1 - 1) mma_commit(&ctl->q_empty);
+          }
+        } else {
+          const int key0 = 128 * (j < ns ? j : t_lo + j - ns);
+          if (key0 + 128 > kvl && kvl < g.Nk) zero_rows(sKV + st * C::TILE, PART, C::PARTS, kvl - key0, 128);
+          if (key0 < dead_lo && key0 + 128 > dead_sk)
+            zero_rows(sKV + st * C::TILE, PART, C::PARTS, dead_sk > key0 ? dead_sk - key0 : 0,
+                      dead_lo - key0 < 128 ? dead_lo - key0 : 128);
+          const bool first = j - j0 < 2;
+          if ((first && items[t] >= 1 &&
+               !mbar_wait_warp(&ctl->o_empty[t], (uint32_t)(items[t] - 1) & 1, abort_flag, a.status, cap)) ||
+              !mbar_wait_warp(&ctl->p_full[t], cnt[t] & 1, abort_flag, a.status, cap)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = umma_desc_sw128(tile_at, PART, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t tP = tS + 32 * (kk >> 1) + 8 * (kk & 1);
+              mma_ts(tO, tP, vd + ((kk * 2048) >> 4), C::IDESC_PV, first && kk == 0 ? 0u : 1u);
+              mma_ts(tO, tP + 16, vd + ((kk * 2048) >> 4), C::IDESC_PV, 1u);
+            }
+            mma_commit(&ctl->pv_done[t]);
+            mma_commit(&ctl->kv_empty[st]);
+            if (j >= j1 - 2) mma_commit(&ctl->o_full[t]);
+          }
+        }
+        __syncwarp();
+        ++cnt[t];
+      }
+      items[0] += 1;
+      items[1] += j1 - j0 > 1;
+      seq += 2ll * (j1 - j0);
+    }
     if (elect_one()) {
       mma_commit(&ctl->drain);
       mbar_drain(&ctl->drain, 0, a.status, cap);
@@ -726,6 +822,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const float alpha = ex2(m_use - m_new);
                   if (over) m = m_new;
                   m_use = m_new;
+                  // (S waited for the PV of the group's step before, so O holds it)
                   scale_o<D>(tO, alpha);
                   l *= alpha;
 #pragma unroll 1
@@ -887,10 +984,10 @@ template <int D, bool DUAL>
 cudaError_t launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                        const WinFwdArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Cfg<D>::SMEM);
+                                       (int)Cfg<D, DUAL>::SMEM);
   if (e != cudaSuccess) return e;
   const int grid = a.n_items < num_sms ? a.n_items : num_sms;
-  window_fwd_kernel<D, DUAL><<<grid, THREADS, Cfg<D>::SMEM, s>>>(mq, mk, mv, mo, a);
+  window_fwd_kernel<D, DUAL><<<grid, THREADS, Cfg<D, DUAL>::SMEM, s>>>(mq, mk, mv, mo, a);
   return cudaGetLastError();
 }
 
