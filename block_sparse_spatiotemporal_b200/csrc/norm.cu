@@ -99,6 +99,12 @@ __device__ inline void team_sync(int warps, int id) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(32 * warps) : "memory");
 }
 
+// 1 / sqrt(v): the approximation (2 steps of fp32 at most) and one Newton step.
+__device__ inline float rsqrt_near(float v) {
+  const float r = rsqrtf(v);
+  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+}
+
 struct Range {
   long long r0, r1;
 };
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
 #pragma unroll
   for (int k = 0; k < RW; ++k) {
     const float mean = s[k] * inv_c;             // of x - x0
-    const float rstd = rsqrtf(fmaf(m2[k], inv_c, a.eps));
+    const float rstd = rsqrt_near(fmaf(m2[k], inv_c, a.eps));
     RS[k] = both(rstd);
     MR[k] = both(-mean * rstd);
     if (L.t == 0 && on[k]) {
