@@ -758,6 +758,102 @@ def run_prologue(args, wl):
     return 0
 
 
+def run_streaming(args, wl):
+    """The attention block of a streaming video model at the workload's shape,
+    one call after another as a step runs them: layer norm of the frames with
+    one scale / shift per frame, QKV projection + RoPE, attention over a
+    window of frames and the first frame.  One JSON line."""
+    import torch
+    from block_sparse_spatiotemporal_b200 import fvattn as F
+    from block_sparse_spatiotemporal_b200.inputs import make_projection_inputs
+
+    dev = torch.device("cuda", 0)
+    B, N, H, d = wl.batch, wl.tokens, wl.heads, wl.head_dim
+    T, frame, C = wl.grid[0], wl.grid[1] * wl.grid[2], wl.heads * wl.head_dim
+    window, sinks = 3, 1
+    x, w, b = make_projection_inputs(B, N, C, H, d, wl.seed)
+    xd = torch.from_numpy(x.view(np.int16)).view(torch.bfloat16).to(dev)
+    wd = torch.from_numpy(w.view(np.int16)).view(torch.bfloat16).to(dev)
+    bd = torch.from_numpy(b).to(dev)
+    gen = torch.Generator(dev).manual_seed(wl.seed)
+    mod = torch.randn(2, B * T, C, device=dev, generator=gen) * 0.2
+    norm = F.make_norm(B * N, C, groups=B * T, gain_one=True)
+    shape = F.make_shape(B, H, d, wl.grid, layout=F.NATURAL)
+    rope = F.make_rope(wl.rope_dims, wl.rope_base)
+    pws = torch.empty(F.workspace_size_qkv(shape, rope), dtype=torch.uint8, device=dev)
+    win = F.make_window(B, H, d, N, N, window, sinks=sinks, unit=frame)
+    ws = F.window_workspace(win, device=dev)
+    y, qkv = torch.empty_like(xd), tuple(torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev) for _ in range(3))
+    out, lse = torch.empty_like(qkv[0]), torch.empty((B, H, N), device=dev)
+    stat = torch.empty(2, B * N, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    pairs = sum(frame * frame * (min(t + 1, window) + min(sinks, max(0, t + 1 - window))) for t in range(T))
+    flops = 4.0 * B * H * d * pairs
+
+    def step(xx=xd):
+        F.layer_norm_fwd(norm, xx, weight=mod[0], bias=mod[1], y=y, mean=stat[0], rstd=stat[1])
+        F.qkv_rope(shape, y, wd, pws, bias=bd, rope=rope, out=qkv)
+        F.window_fwd(win, *qkv, ws, out=out, lse=lse)
+
+    def timed(fn, n):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(n):
+            fn()
+        e1.record(stream)
+        torch.cuda.synchronize(dev)
+        return e0.elapsed_time(e1) / n
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize(dev)
+    if F.device_status(ws) != 0 or F.device_status(pws) != 0:
+        raise RuntimeError("device status set during warm-up")
+    sampler = ClockSampler([0])
+    sampler.start()
+    time.sleep(0.3)
+    F.profile_read()
+    F.profile_enable(True)
+    ms = timed(step, args.steps)
+    F.profile_enable(False)
+    stages = F.profile_read()
+    clocks = sampler.stop()
+    if F.device_status(ws) != 0 or F.device_status(pws) != 0:
+        raise RuntimeError("device status set during the timed region")
+
+    xh = torch.from_numpy(x.view(np.int16)).view(torch.bfloat16).pin_memory()
+    oh = torch.empty(out.shape, dtype=torch.bfloat16).pin_memory()
+    xb = torch.empty_like(xd)
+
+    def e2e_step():
+        xb.copy_(xh, non_blocking=True)
+        step(xb)
+        oh.copy_(out, non_blocking=True)
+    for _ in range(2):
+        e2e_step()
+    torch.cuda.synchronize(dev)
+    e2e_ms = timed(e2e_step, max(3, min(args.steps, 10)))
+
+    pk, pk_kind = peaks()
+    w_ms, w_n = stages["window"]
+    achieved = flops / (w_ms / max(w_n, 1) / 1e3) / 1e12
+    print(json.dumps({
+        "metric": "streaming attention block ms (norm + QKV/RoPE + windowed attention)", "value": ms, "unit": "ms",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": False,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"streaming_{wl.name}", "grid": list(wl.grid), "tokens": N, "channels": C, "heads": H,
+                   "head_dim": d, "frame_tokens": frame, "window_frames": window, "sink_frames": sinks,
+                   "l2": "inputs larger than L2"},
+        "stage_ms": {k: round(v[0] / args.steps, 4) for k, v in stages.items() if v[1]},
+        "roofline": {"kernel": "window_fwd_kernel", "bound": "tensor", "achieved": achieved, "peak": pk["bf16_tflops"],
+                     "unit": "TFLOP/s", "frac": achieved / pk["bf16_tflops"], "traffic": None,
+                     "peak_source": f"{pk_kind} bf16 burst"},
+        "gpu_launches": sum(n for _, n in stages.values()), "clocks": clocks,
+        "e2e": {"value": e2e_ms, "unit": "ms", "ms_per_step": e2e_ms, "h2d_bytes_per_step": xh.numel() * 2,
+                "d2h_bytes_per_step": oh.numel() * 2}}), flush=True)
+    return 0
+
+
 def run_backward(args, wl):
     """The fine-stage backward at the workload's shape: lists from the
     library's own selection, out / lse from its forward, a seeded dout, all
@@ -1019,6 +1115,8 @@ def main():
                     help="hierarchical sub-block scoring (pool_select_subblock + block_sparse_fwd)")
     ap.add_argument("--prologue", action="store_true",
                     help="the fused QKV projection + 3D RoPE prologue at the workload's shape (one JSON line)")
+    ap.add_argument("--streaming", action="store_true",
+                    help="layer norm, projection and windowed attention of a streaming step (one JSON line)")
     ap.add_argument("--backward", action="store_true",
                     help="the fine-stage backward (dq, dk, dv) at the workload's shape (one JSON line)")
     ap.add_argument("--augment", action="store_true",
@@ -1034,6 +1132,8 @@ def main():
         return run_sweep(args)
     if args.prologue:
         return run_prologue(args, wl)
+    if args.streaming:
+        return run_streaming(args, wl)
     if args.backward:
         return run_backward(args, wl)
     if args.augment:

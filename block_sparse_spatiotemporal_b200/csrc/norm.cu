@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
     const float mean = s[k] * inv_c;             // of x - x0
     const float rstd = rsqrt_near(fmaf(m2[k], inv_c, a.eps));
     RS[k] = both(rstd);
-    MR[k] = both(-mean * rstd);
+    MR[k] = both(sizeof(T) == 4 ? -mean : -mean * rstd);
     if (L.t == 0 && on[k]) {
       if (a.mean_out) a.mean_out[r0 + k] = x0[k] + mean;
       if (a.rstd_out) a.rstd_out[r0 + k] = rstd;
@@ -397,7 +397,12 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) o[i] = fma2(fma2(d[k][c * NP + i], RS[k], MR[k]), w[i], b[i]);
+      for (int i = 0; i < NP; ++i) {
+        const uint64_t e = d[k][c * NP + i];
+        // fp32 keeps the difference exact to its own rounding; a bf16 output does not need the operation
+        const uint64_t xh = sizeof(T) == 4 ? mul2(add2(e, MR[k]), RS[k]) : fma2(e, RS[k], MR[k]);
+        o[i] = fma2(xh, w[i], b[i]);
+      }
       if (on[k]) ch.put(y + (r0 + k) * a.y_stride, c, o);
     }
   }
@@ -685,13 +690,16 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Largest vector (elements) that divides the row and both row strides.
+// Largest vector (elements) that divides the row and both row strides; gain
+// and bias, read four at a time with vectors of four or more, have to be
+// 16-byte aligned for those (their pointers need only be a float's).
 template <typename T>
 int vec_of(const NormArgs& a) {
+  const bool quads = ((reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.b)) & 15) == 0;
   const int opts_b[4] = {8, 4, 2, 1}, opts_f[4] = {4, 1, 1, 1};
   for (int i = 0; i < 4; ++i) {
     const int v = sizeof(T) == 2 ? opts_b[i] : opts_f[i];
-    if (a.C % v == 0 && a.x_stride % v == 0 && a.y_stride % v == 0) return v;
+    if (a.C % v == 0 && a.x_stride % v == 0 && a.y_stride % v == 0 && (quads || v < 4)) return v;
   }
   return 1;
 }

@@ -120,6 +120,25 @@ def test_strided_rows(C, xs, ys, dtype):
     check_bwd(*F.layer_norm_bwd(norm, x, dy, mean, rstd, F.norm_workspace(norm), weight=w), r, DT[dtype][2])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [64, 512, 5120])
+def test_gain_and_bias_at_a_floats_alignment(C, dtype):
+    """weight and bias that start 4 bytes into a 16-byte line (a slice of a
+    larger buffer), and per-row statistics likewise."""
+    rows, groups = 21, 3
+    x, w0, b0, dy = make(rows, C, groups, dtype, 6)
+    buf = torch.empty(2, groups * C + 1, device="cuda")
+    w, b = (buf[i, 1:].view(groups, C) for i in range(2))
+    w.copy_(w0), b.copy_(b0)
+    assert w.data_ptr() % 16 == 4
+    norm = F.make_norm(rows, C, groups, dtype=DT[dtype][1])
+    stat = torch.empty(2, rows + 1, device="cuda")
+    y, mean, rstd = F.layer_norm_fwd(norm, x, weight=w, bias=b, mean=stat[0, 1:], rstd=stat[1, 1:])
+    r = plain(x, w0, b0, dy, groups, 1e-6, False)
+    check_fwd(y, mean, rstd, r, x, DT[dtype][2])
+    check_bwd(*F.layer_norm_bwd(norm, x, dy, mean, rstd, F.norm_workspace(norm), weight=w), r, DT[dtype][2])
+
+
 @pytest.mark.parametrize("C", [96, 1536, 10000])
 def test_in_place_and_single_gradients(C):
     rows, groups = 50, 2
