@@ -389,11 +389,11 @@ struct JoinRows {
       out(row, d0, acc[0]);
     } else {
 #pragma unroll 1
-      for (int row = rb + r / TPR; row < re; row += 4 * RPP) {
-        float acc[4][4];
-        some<D, 4, 2>(sh, rb, re, row, d0, acc);
+      for (int row = rb + r / TPR; row < re; row += 8 * RPP) {
+        float acc[8][4];
+        some<D, 8, 3>(sh, rb, re, row, d0, acc);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (row + k * RPP < re) out(row + k * RPP, d0, acc[k]);
       }
     }
