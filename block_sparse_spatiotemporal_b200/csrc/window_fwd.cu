@@ -93,7 +93,7 @@ struct Item {
 };
 
 struct FwdCtl {
-  uint64_t item_full[ITEMS], item_empty[ITEMS];   // the MMA warps and 8 softmax warps read an item
+  uint64_t item_full[ITEMS], item_empty[ITEMS];   // the warps behind the producer read an item
   uint64_t q_full, q_empty;
   uint64_t kv_full[MAXST], kv_empty[MAXST];
   uint64_t s_full[2];      // S_g of its next step written (and every earlier MMA of the tile complete)
@@ -102,6 +102,7 @@ struct FwdCtl {
   uint64_t o_full[2];      // the item's last PV of tile g complete
   uint64_t o_empty[2];     // O_g read (4 warps)
   uint64_t group[2];       // softmax group t meets (4 warps)
+  uint64_t ready[ITEMS];   // single form, four copies: the item's parts written (8 warps)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -304,10 +305,10 @@ __device__ inline void store_rows(uint8_t* stage, const uint32_t (&v)[32], uint8
   __syncwarp();
 }
 
-// Joining the parts of `rows` rows by 128 threads.  What other SMs wrote is
+// Joining the parts of `rows` rows by NT threads (r: this one's number).  What other SMs wrote is
 // about 1,000 clocks away, so every step asks for several values before it
 // uses one (one after another, 24 parts of 4 rows took 25,000 clocks).
-struct JoinRows {
+template <int NT> struct JoinRows {
   const float *lse, *o;   // part 0 of row 0
   long long step;         // rows from a part to the next
   int parts, rows;
@@ -316,16 +317,16 @@ struct JoinRows {
   __device__ void load_lse(float* sh, int rb, int re, int r) const {
     const int n = (re - rb) * parts;
 #pragma unroll 1
-    for (int e0 = r; e0 < n; e0 += 4 * 128) {
+    for (int e0 = r; e0 < n; e0 += 4 * NT) {
       float v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int e = e0 + 128 * k < n ? e0 + 128 * k : e0;
+        const int e = e0 + NT * k < n ? e0 + NT * k : e0;
         v[k] = __ldcg(lse + (e % parts) * step + rb + e / parts);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (e0 + 128 * k < n) sh[e0 + 128 * k] = v[k];
+        if (e0 + NT * k < n) sh[e0 + NT * k] = v[k];
     }
   }
   // one row's parts to their shares 2^(lse_p - max) / sum; returns its lse (natural)
@@ -348,7 +349,7 @@ struct JoinRows {
   // NR rows x NP parts at a time: rows row, row + RPP, ..
   template <int D, int NR, int NP>
   __device__ void some(const float* sh, int rb, int re, int row, int d0, float (&acc)[NR][4]) const {
-    constexpr int RPP = 512 / D;
+    constexpr int RPP = 4 * NT / D;
     int up[NR];
 #pragma unroll
     for (int k = 0; k < NR; ++k) {
@@ -379,21 +380,22 @@ struct JoinRows {
   }
   // out(row, first dim, four dims) for rows rb .. re - 1
   template <int D, typename F> __device__ void sum(const float* sh, int rb, int re, int r, F out) const {
-    constexpr int TPR = D / 4, RPP = 128 / TPR;        // threads a row, rows a pass
+    constexpr int TPR = D / 4, RPP = NT / TPR;         // threads a row, rows a pass
     const int d0 = (r % TPR) * 4;
-    if (re - rb <= RPP) {
-      const int row = rb + r / TPR;
-      if (row >= re) return;
-      float acc[1][4];
-      some<D, 1, 8>(sh, rb, re, row, d0, acc);
-      out(row, d0, acc[0]);
+    if (NT == 32 || re - rb <= RPP) {
+#pragma unroll 1
+      for (int row = rb + r / TPR; row < re; row += RPP) {
+        float acc[1][4];
+        some<D, 1, 8>(sh, rb, re, row, d0, acc);
+        out(row, d0, acc[0]);
+      }
     } else {
 #pragma unroll 1
-      for (int row = rb + r / TPR; row < re; row += 8 * RPP) {
-        float acc[8][4];
-        some<D, 8, 3>(sh, rb, re, row, d0, acc);
+      for (int row = rb + r / TPR; row < re; row += 4 * RPP) {
+        float acc[4][4];
+        some<D, 4, 2>(sh, rb, re, row, d0, acc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 4; ++k)
           if (row + k * RPP < re) out(row + k * RPP, d0, acc[k]);
       }
     }
@@ -421,7 +423,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], DUAL ? 9 : 10);
+      mbar_init(&ctl->item_empty[i], DUAL ? 9 : 11);
+      mbar_init(&ctl->ready[i], 8);
     }
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->q_empty, 1);
@@ -712,6 +715,57 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_drain(&ctl->drain, 0, a.status, cap);
     }
     __syncwarp();
+  } else if (!DUAL && warp == 3) {
+    // ---------------------------------------- joins the parts of few rows
+    // (a quarter of the softmax warps' time an item went into the fence, the
+    // counter and the join, with the next item's K and V waiting)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const int prow = a.tokens * a.pack;
+    for (int n = 0;; ++n) {
+      const int ib = n % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item& si = ctl->item[ib];
+      const int idx = si.idx, split = si.split, batch = si.b, head0 = si.hk * g.G + si.g0, tok0 = si.tile * a.tokens;
+      const int left = si.seq.ql - tok0;
+      if (idx < 0 || a.copies < 4) {             // the groups join larger items themselves
+        mbar_arrive_warp(&ctl->item_empty[ib]);
+        if (idx < 0) break;
+        continue;
+      }
+      if (!mbar_wait_warp(&ctl->ready[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const int base = idx - split;
+      int last = 0;
+      if (lane == 0) {
+        __threadfence();
+        last = atomicAdd(a.counters + base / a.splits, 1) == a.splits - 1;
+      }
+      last = __shfl_sync(0xffffffffu, last, 0);
+      if (last) {
+        __threadfence();
+        const int rows = (left < a.tokens ? left : a.tokens) * a.pack;
+        const JoinRows<32> jr{a.part_lse + (long long)base * 8 * prow, a.part_o + (long long)base * 8 * prow * D, prow,
+                              a.parts, rows};
+        float* share = reinterpret_cast<float*>(sOut);         // [batch of rows][parts]
+        const int most = (int)(8 * OUT_STAGE / sizeof(float)) / a.parts;
+        for (int rb = 0; rb < rows; rb += most) {
+          const int re = rb + most < rows ? rb + most : rows;
+          jr.load_lse(share, rb, re, lane);
+          __syncwarp();
+          for (int row = rb + lane; row < re; row += 32)
+            a.lse[((long long)batch * g.H + head0 + row % a.pack) * g.Nq + tok0 + row / a.pack] =
+                jr.shares(share + (row - rb) * a.parts);
+          __syncwarp();
+          jr.template sum<D>(share, rb, re, lane, [&](int rr, int d0, const float (&v)[4]) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
+                                 (long long)(head0 + rr % a.pack) * a.o_head + (long long)(tok0 + rr / a.pack) * a.o_token +
+                                 d0;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+          });
+          __syncwarp();
+        }
+      }
+      mbar_arrive_warp(&ctl->item_empty[ib]);    // behind the join: the ready barriers stay an item apart
+    }
   } else if (warp < SW0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   } else {
@@ -923,7 +977,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         mbar_arrive_warp(&ctl->o_empty[t]);
       }
-      if (parts) {
+      if (!DUAL && copies == 4) {
+        mbar_arrive_warp(&ctl->ready[ib]);       // the joining warp takes it from here
+      } else if (parts) {
         // the group that completes the query tile's parts joins them
         __threadfence();
         mbar_arrive_warp(&ctl->group[t]);
@@ -940,7 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // part p of a row: split p of this tile, or copy p % copies of group (p / copies) % 2 of its split
           const long long row0 = (long long)base * 2 * copies * prow + (DUAL ? t * prow : 0);
           const long long step = (DUAL ? 2ll : 1ll) * prow;
-          const JoinRows jr{a.part_lse + row0, a.part_o + row0 * D, step, a.parts, rows};
+          const JoinRows<128> jr{a.part_lse + row0, a.part_o + row0 * D, step, a.parts, rows};
           float* share = reinterpret_cast<float*>(sOut + t * 4 * OUT_STAGE);        // [batch of rows][parts]
           const int most = (int)(4 * OUT_STAGE / sizeof(float)) / a.parts;
           bool joined = true;
