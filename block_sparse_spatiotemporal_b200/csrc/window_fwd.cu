@@ -872,7 +872,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const bool over = again == 0 && valid && !(sum <= RESCALE_SUM);
                   if (!__any_sync(0xffffffffu, over)) break;
                   // as above; what this step already holds of P moves too
-                  const float m_new = over ? fmaxf(max_chunk(tC, sp, k0) * sl2, m_use) : m_use;
+                  const float mx = fmaxf(max_chunk(tC, sp, k0) * sl2, m_use);   // by every lane: TMEM loads are the warp's
+                  const float m_new = over ? mx : m_use;
                   const float alpha = ex2(m_use - m_new);
                   if (over) m = m_new;
                   m_use = m_new;

@@ -126,6 +126,47 @@ def test_large_logits_move_the_reference(Nq):
     check(out, lse, plain_fwd(q, k, v, 1, 0, 0))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Nq", [3, 40, 100, 130, 260])
+def test_reference_moves_inside_a_tile(Nq, D):
+    """Logits that jump by more than 2^64 every 32 keys, up and down again, in
+    every form: rows held four times, twice and once, and two query tiles."""
+    B, H, Nk = 1, 1, 600
+    gen = torch.Generator("cuda").manual_seed(8)
+    q = torch.ones(B, H, Nq, D, dtype=torch.bfloat16, device="cuda")
+    steps = torch.arange(Nk, device="cuda") // 32
+    ramp = torch.where(steps < 12, steps, 24 - steps) * (128.0 / D)
+    k = heads(gen, B, H, Nk, D, mul=0.02) + (ramp * 8.0)[:, None].to(torch.bfloat16)
+    v = heads(gen, B, H, Nk, D)
+    for window, sinks in ((0, 0), (200, 40)):
+        win = F.make_window(B, H, D, Nq, Nk, window, sinks=sinks)
+        out, lse = run(win, q, k, v)
+        check_far(out, lse, plain_fwd(q, k, v, 1, window, sinks))
+
+
+def check_far(out, lse, ref):
+    """check() for logits of size s: one fp32 rounding of s, relative 2^-24,
+    is |s| 2^-24 of a logit, which the probabilities and lse carry as
+    ln 2 times as much; here |s| < 2^12, so 2^-11 of both covers it."""
+    want, wl, spread = ref
+    err = (out.double() - want).abs()
+    assert (err <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11) * spread).all(), float(err.max())
+    assert ((lse.double() - wl).abs() <= 2.0 ** -11 * (1 + wl.abs() * 2.0 ** -9)).all()
+
+
+@pytest.mark.parametrize("unit,window,sinks", [(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1, 0), (3, 1, 2 ** 31 - 1),
+                                               (2 ** 31 - 1, 1, 0), (7, 2, 50)])
+def test_extreme_parameters(unit, window, sinks):
+    B, H, D, Nq, Nk = 1, 2, 64, 150, 200
+    gen = torch.Generator("cuda").manual_seed(9)
+    q, k, v = (heads(gen, B, H, n, D) for n in (Nq, Nk, Nk))
+    win = F.make_window(B, H, D, Nq, Nk, window, sinks=sinks, unit=unit)
+    out, lse = run(win, q, k, v)
+    # what does not fit the plain form's sizes is more than there is: the same as 10^6
+    cut = [min(x, 10 ** 6) for x in (unit, window, sinks)]
+    check(out, lse, plain_fwd(q, k, v, *cut))
+
+
 def test_scale_and_stream_and_graph():
     """A given scale, a side stream, and a captured call that is replayed on
     new inputs, a split one (few queries) among them."""

@@ -108,6 +108,16 @@ def test_padded_batch(D):
             assert (g[b, :, lens[b]:] == 7).all()
 
 
+@pytest.mark.parametrize("unit,window,sinks", [(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1), (3, 1, 2 ** 31 - 1), (2 ** 31 - 1, 1, 0)])
+def test_extreme_parameters(unit, window, sinks):
+    B, H, D, Nq, Nk = 1, 2, 64, 150, 200
+    gen = torch.Generator("cuda").manual_seed(9)
+    q, dout, k, v = (heads(gen, B, H, n, D) for n in (Nq, Nq, Nk, Nk))
+    win = F.make_window(B, H, D, Nq, Nk, window, sinks=sinks, unit=unit)
+    cut = [min(x, 10 ** 6) for x in (unit, window, sinks)]
+    check(run(win, q, k, v, dout), plain_bwd(q, k, v, dout, *cut))
+
+
 def test_gradient_against_differences():
     """Central differences of the plain 64-bit forward along random
     directions: the bf16 gradients have to give the same slopes."""
