@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int j = it.j0; j < it.j1; ++j, ++c) {
         const int b = (int)(c % NB), st = (int)(c % MST);
-        if (!mbar_wait(&ctl->s_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap)) {
+        if (!mbar_wait_warp(&ctl->s_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap)) {
           ok = false;
           break;
         }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       // ---- epilogue: accumulators to bf16 rows, or to this part's place in the workspace
       if (steps) {
-        if (!mbar_wait(&ctl->acc_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->acc_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
         ++k;
         tc_fence_after();
       }
@@ -547,10 +547,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the last of the tile's parts to arrive adds them in ascending order
         __threadfence();
         mbar_arrive_warp(&ctl->meet);
-        if (!mbar_wait(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
         if (threadIdx.x == CW0 * 32) ctl->last = atomicAdd(a.counters + it.cell, 1) == it.parts - 1;
         mbar_arrive_warp(&ctl->meet);
-        if (!mbar_wait(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
         if (ctl->last) {
           __threadfence();
           const float* src = a.part + (long long)(idx - it.part) * 2 * 128 * D;

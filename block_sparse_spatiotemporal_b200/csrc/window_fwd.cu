@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int ib = n % ITEMS;
-      if (!mbar_wait(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
       const Item& si = ctl->item[ib];
       const int idx = si.idx, j0 = si.j0, j1 = si.j1, ns = si.ns, t_lo = si.t_lo, split = si.split;
       const int batch = si.b, head0 = si.hk * g.G + si.g0, tok0 = (si.tile + (DUAL ? t : 0)) * a.tokens;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = j0; j < j1; ++j) {
         const int kt = j < ns ? j : t_lo + j - ns;
         if (!turn.on(j, kt)) continue;
-        if (!mbar_wait(&ctl->s_full[t], cnt & 1, abort_flag, a.status, cap)) {
+        if (!mbar_wait_warp(&ctl->s_full[t], cnt & 1, abort_flag, a.status, cap)) {
           ok = false;
           break;
         }
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       // ---- epilogue
       if (any) {
-        if (!mbar_wait(&ctl->o_full[t], (uint32_t)items & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->o_full[t], (uint32_t)items & 1, abort_flag, a.status, cap)) break;
         tc_fence_after();
         ++items;
       }
@@ -984,12 +984,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the group that completes the query tile's parts joins them
         __threadfence();
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
         const int base = idx - split;                  // split 0 of this item
         if (r == 0)
           ctl->last[t] = atomicAdd(a.counters + (DUAL ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts / copies - 1;
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+        if (!mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
         if (ctl->last[t]) {
           __threadfence();
           const int left = seq.ql - tok0;
@@ -1005,14 +1005,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int re = rb + most < rows ? rb + most : rows;
             jr.load_lse(share, rb, re, r);
             mbar_arrive_warp(&ctl->group[t]);
-            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
             if (!joined) break;
             const int row = rb + r;
             if (row < re)
               a.lse[((long long)batch * g.H + head0 + row % a.pack) * g.Nq + tok0 + row / a.pack] =
                   jr.shares(share + r * a.parts);
             mbar_arrive_warp(&ctl->group[t]);
-            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
             if (!joined) break;
             jr.template sum<D>(share, rb, re, r, [&](int rr, int d0, const float (&v)[4]) {
               __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
             });
             mbar_arrive_warp(&ctl->group[t]);          // the shares are read
-            joined = mbar_wait(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
           }
           if (!joined) break;
         }
