@@ -838,9 +838,9 @@ WinBwdWs win_bwd_ws(const WinGeom& g, const WinBwdPlan& p) {
   const size_t rows = align_up(sizeof(float) * (size_t)g.B * g.H * g.Nq);
   const bool split = p.heavy_parts > 1 || p.parts > 1;
   WinBwdWs L{};
-  L.counters = kAlign;               // behind the status word
+  L.counters = kAlign;               // behind the status word and the two kernels' item counters
   const size_t n = split ? sizeof(int) * (size_t)g.B * g.Hk * p.tiles : 0;
-  L.zeroed = split ? L.counters + n : sizeof(int);
+  L.zeroed = split ? L.counters + n : 3 * sizeof(int);
   L.lse2 = align_up(L.counters + n);
   L.dd = L.lse2 + rows;
   L.part = L.dd + rows;
@@ -1419,6 +1419,7 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     a.n_items = plan.n_items;
     a.part = reinterpret_cast<float*>(base + L.part);
     a.counters = reinterpret_cast<int*>(base + L.counters);
+    a.next_item = a.status + 1;
     a.out0 = WinOut{dk->data, dk->batch, dk->head, dk->token};
     a.out1 = WinOut{dv->data, dv->batch, dv->head, dv->token};
     StageTimer t(FVATTN_STAGE_WINDOW_KV, s);
@@ -1432,6 +1433,7 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     FV_TRY(make_head_map(&m3, *v, g, g.Hk, g.Nk, 64, any));
     a.tiles = q_tiles;
     a.n_items = g.B * g.H * q_tiles;
+    a.next_item = a.status + 2;
     a.out0 = WinOut{dq->data, dq->batch, dq->head, dq->token};
     StageTimer t(FVATTN_STAGE_WINDOW_Q, s);
     FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, false, dev.sms, s));

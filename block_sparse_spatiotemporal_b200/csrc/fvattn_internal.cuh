@@ -233,6 +233,7 @@ struct WinBwdArgs {
   float* part;                     //   [n_items][2][128][D] sums of the parts
   int* counters;                   //   parts written, per (batch, KV head, tile), zeroed
   int n_items;
+  int* next_item;                  // zeroed: items handed out after each CTA's first
   const float* lse2;               // [B, H, Nq] lse * log2(e)
   const float* dd;                 // [B, H, Nq] rowsum(dout * out)
   WinOut out0;                     // dK (key-stationary) or dQ

@@ -58,26 +58,11 @@ template <bool KV> struct Tm {
 };
 constexpr int MAXNB = 3;
 
-struct Ctl {
-  uint64_t stat_full, stat_empty;
-  uint64_t mov_full[MAXST], mov_empty[MAXST];
-  uint64_t s_full[MAXNB];    // S and dP of step c in buffer c % NB (two commits)
-  uint64_t p_full[MAXNB];    // P / dS of step c written back (8 warps)
-  uint64_t step_done[MAXNB]; // the accumulating MMAs of step c, which read buffer c % NB, complete
-  uint64_t acc_full;         // the item's accumulators complete
-  uint64_t acc_empty;        // the epilogue read them (8 warps)
-  uint64_t meet;             // the compute warps meet (8 warps)
-  uint64_t drain;
-  alignas(16) float lse2[MAXST][64];     // key-stationary only: lse * log2(e) of the step's queries
-  alignas(16) float dd[MAXST][64];       //   and their rowsum(dout * out)
-  uint32_t tmem_base;
-  int abort;
-  int last;                  // this part was its tile's last
-};
-static_assert(Sh<128>::SMEM + sizeof(Ctl) <= 232448 && Sh<64>::SMEM + sizeof(Ctl) <= 232448, "shared memory");
+constexpr int ITEMS = 2;      // items published ahead
 
-// A work item and its steps, the same for every warp.
+// A work item and its steps.
 template <bool KV> struct Item {
+  int idx;               // -1: the CTA has no further item
   int b, hk, h;          // h: query head (query-stationary)
   int row0;              // first stationary row (key or query)
   Seq seq;
@@ -94,6 +79,7 @@ template <bool KV> struct Item {
 template <bool KV> __device__ inline Item<KV> item_of(const WinBwdArgs& a, int idx) {
   const WinGeom& g = a.g;
   Item<KV> it{};
+  it.idx = idx;
   if (KV) {
     // the tiles with sinks first: every later query sees them
     const int heavy = a.heavy_tiles * g.B * g.Hk * a.heavy_parts;
@@ -169,6 +155,26 @@ template <bool KV> __device__ inline Item<KV> item_of(const WinBwdArgs& a, int i
   return it;
 }
 
+template <bool KV> struct Ctl {
+  uint64_t item_full[ITEMS], item_empty[ITEMS];   // 3 MMA and 8 compute warps read an item
+  uint64_t stat_full, stat_empty;
+  uint64_t mov_full[MAXST], mov_empty[MAXST];
+  uint64_t s_full[MAXNB];    // S and dP of step c in buffer c % NB (two commits)
+  uint64_t p_full[MAXNB];    // P / dS of step c written back (8 warps)
+  uint64_t step_done[MAXNB]; // the accumulating MMAs of step c, which read buffer c % NB, complete
+  uint64_t acc_full;         // the item's accumulators complete
+  uint64_t acc_empty;        // the epilogue read them (8 warps)
+  uint64_t meet;             // the compute warps meet (8 warps)
+  uint64_t drain;
+  alignas(16) float lse2[MAXST][64];     // key-stationary only: lse * log2(e) of the step's queries
+  alignas(16) float dd[MAXST][64];       //   and their rowsum(dout * out)
+  Item<KV> item[ITEMS];
+  uint32_t tmem_base;
+  int abort;
+  int last;                  // this part was its tile's last
+};
+static_assert(Sh<128>::SMEM + sizeof(Ctl<true>) <= 232448 && Sh<64>::SMEM + sizeof(Ctl<true>) <= 232448, "shared memory");
+
 // K-major operand of 64-dim parts `part` bytes apart, K step kk.
 __device__ inline uint64_t kdesc(uint32_t base, uint32_t part, int kk) {
   return umma_desc_sw128(base + (kk >> 2) * part + (kk & 3) * 32, 16, 1024);
@@ -185,14 +191,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sStat = smem;                         // X0 then X1
   uint8_t* sMov = smem + C::STAT_BYTES;          // per stage: Y0 then Y1
-  __shared__ Ctl ctl_s;
-  Ctl* ctl = &ctl_s;
+  __shared__ Ctl<KV> ctl_s;
+  Ctl<KV>* ctl = &ctl_s;
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WinGeom& g = a.g;
   const long long cap = a.wait_cap;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&ctl->item_full[i], 1);
+      mbar_init(&ctl->item_empty[i], 3 + CTHREADS / 32);
+    }
     mbar_init(&ctl->stat_full, 1);
     mbar_init(&ctl->stat_empty, 2);              // one commit per score warp
     for (int i = 0; i < MST; ++i) {
@@ -232,8 +242,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     long long gs = 0;       // moving steps loaded
     int k = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item<KV> it = item_of<KV>(a, idx);
+    int idx = blockIdx.x;   // then the next one from a counter
+    for (int n = 0; ok; ++n) {
+      const int ib = n % ITEMS;
+      if (n >= ITEMS &&
+          !mbar_wait_warp(&ctl->item_empty[ib], (uint32_t)(n / ITEMS - 1) & 1, abort_flag, a.status, cap))
+        break;
+      if (leader) {
+        if (idx < a.n_items) {
+          ctl->item[ib] = item_of<KV>(a, idx);
+          idx = gridDim.x + atomicAdd(a.next_item, 1);
+        } else {
+          ctl->item[ib].idx = -1;
+        }
+        mbar_arrive(&ctl->item_full[ib]);
+      }
+      __syncwarp();
+      const Item<KV> it = ctl->item[ib];     // overwritten only when this warp comes round again
+      if (it.idx < 0) break;
       if (it.j0 == it.j1) continue;
       if (leader) {
         if (k >= 1) ok = mbar_wait(&ctl->stat_empty, (uint32_t)(k - 1) & 1, abort_flag, a.status, cap);
@@ -297,9 +323,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     const uint32_t x = smem_u32(sStat) + (is_s ? 0u : C::STENSOR);
     const uint32_t tdst = tbase + (is_s ? Tm<KV>::S : Tm<KV>::DP);
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item<KV> it = item_of<KV>(a, idx);
-      const int n = it.j1 - it.j0;
+    for (int m = 0; ok; ++m) {
+      const int ib = m % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(m / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const int idx = ctl->item[ib].idx, n = ctl->item[ib].j1 - ctl->item[ib].j0;
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      if (idx < 0) break;
       if (n == 0) continue;
       if (!mbar_wait_warp(&ctl->stat_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
       ++k;
@@ -334,8 +363,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     long long c = 0;
     int k = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item<KV> it = item_of<KV>(a, idx);
+    for (int m = 0; ok; ++m) {
+      const int ib = m % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(m / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item<KV> it = ctl->item[ib];
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      if (it.idx < 0) break;
       if (it.j0 == it.j1) continue;
       if (k >= 1 && !mbar_wait_warp(&ctl->acc_empty, (uint32_t)(k - 1) & 1, abort_flag, a.status, cap)) break;
       ++k;
@@ -401,8 +434,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     int k = 0;
     uint32_t meets = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; idx < a.n_items && ok; idx += gridDim.x) {
-      const Item<KV> it = item_of<KV>(a, idx);
+    for (int m = 0; ok; ++m) {
+      const int ib = m % ITEMS;
+      if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(m / ITEMS) & 1, abort_flag, a.status, cap)) break;
+      const Item<KV> it = ctl->item[ib];
+      mbar_arrive_warp(&ctl->item_empty[ib]);
+      const int idx = it.idx;
+      if (idx < 0) break;
       const int row = it.row0 + r;
       const bool valid = row < (KV ? it.seq.kvl : it.seq.ql);
       // moving rows this row meets: KV: queries [lo, hi); else keys [lo, hi) and [0, sk)
