@@ -1388,7 +1388,7 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
   FV_TRY(device_info(&dev));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
-  FV_CUDA(cudaMemsetAsync(base, 0, L.zeroed, s));
+  if (g.Nq == 0) FV_CUDA(cudaMemsetAsync(base, 0, L.zeroed, s));   // otherwise prep does it
   if (g.Nq == 0 && g.Nk == 0) return FVATTN_OK;
   // a tensor without rows has no address: its maps, which no load uses, take another's
   const void* any = g.Nq > 0 ? q->data : k->data;
@@ -1397,7 +1397,8 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
   const WinOut wo{out->data, out->batch, out->head, out->token}, wd{dout->data, dout->batch, dout->head, dout->token};
   if (g.Nq > 0) {
     StageTimer t(FVATTN_STAGE_WINDOW_PREP, s);
-    FV_CUDA(launch_window_prep(g, wo, wd, lse, lse2, dd, s));
+    FV_CUDA(launch_window_prep(g, wo, wd, lse, lse2, dd, reinterpret_cast<int*>(base),
+                               (long long)(L.zeroed / sizeof(int)), s));
     t.kernels = 1;
   }
   WinBwdArgs a{};
@@ -1423,7 +1424,7 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     a.out0 = WinOut{dk->data, dk->batch, dk->head, dk->token};
     a.out1 = WinOut{dv->data, dv->batch, dv->head, dv->token};
     StageTimer t(FVATTN_STAGE_WINDOW_KV, s);
-    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, true, dev.sms, s));
+    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, true, g.Nq > 0 && !t.a, dev.sms, s));
     t.kernels = 1;
   }
   if (g.Nq > 0) {
@@ -1436,7 +1437,7 @@ int fvattn_window_bwd(const fvattn_window* win, const fvattn_view* q, const fvat
     a.next_item = a.status + 2;
     a.out0 = WinOut{dq->data, dq->batch, dq->head, dq->token};
     StageTimer t(FVATTN_STAGE_WINDOW_Q, s);
-    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, false, dev.sms, s));
+    FV_CUDA(launch_window_bwd(m0, m1, m2, m3, a, false, g.Nk > 0 && !t.a, dev.sms, s));
     t.kernels = 1;
   }
   return FVATTN_OK;

@@ -635,10 +635,10 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int dtype, const void* x, const v
 cudaError_t launch_window_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                               const WinFwdArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_window_prep(const WinGeom& g, const WinOut& out, const WinOut& dout, const float* lse, float* lse2,
-                               float* dd, cudaStream_t s);
+                               float* dd, int* words, long long zeroed, cudaStream_t s);
 cudaError_t launch_window_bwd(const CUtensorMap& s0, const CUtensorMap& s1, const CUtensorMap& m0,
-                              const CUtensorMap& m1, const WinBwdArgs& a, bool key_stationary, int num_sms,
-                              cudaStream_t s);
+                              const CUtensorMap& m1, const WinBwdArgs& a, bool key_stationary, bool early,
+                              int num_sms, cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, long long cap, cudaStream_t s);
 
 }  // namespace fvattn

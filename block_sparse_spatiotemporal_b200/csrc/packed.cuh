@@ -40,17 +40,11 @@ __device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ inline uint64_t add2_rm(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ inline uint64_t sub2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ inline uint64_t neg2(uint64_t a) { return a ^ 0x8000000080000000ull; }
 __device__ inline uint64_t both(float v) { return f2(v, v); }
 __device__ inline float sum2(uint64_t a) {
   float lo, hi;

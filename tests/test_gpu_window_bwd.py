@@ -167,3 +167,40 @@ def test_side_stream_and_graph():
         torch.cuda.synchronize()
         assert F.device_status(ws) == 0
         check(got, plain_bwd(q, k, v, dout, 1, 100, 4))
+
+
+def test_calls_one_behind_another():
+    """The kernels of a call overlap; calls that share a workspace and reads
+    of the gradients behind each must not: the bits of a run alone."""
+    cases = []
+    for seed, (H, Hk, D, N, window) in enumerate([(4, 2, 128, 700, 150), (14, 2, 64, 515, 90), (2, 2, 128, 70, 0)]):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        q, k, v, dout = (heads(gen, 1, n, N, D) for n in (H, Hk, Hk, H))
+        win = F.make_window(1, H, D, N, N, window, sinks=5 if window else 0, kv_heads=Hk)
+        own = F.window_workspace(win, backward=True)
+        out, lse = F.window_fwd(win, q, k, v, own)
+        args = (q, k, v, out, dout, lse)
+        alone = F.window_bwd(win, *args, own)
+        torch.cuda.synchronize()
+        cases.append((win, args, alone))
+    ws = max((F.window_workspace(c[0], backward=True) for c in cases), key=lambda t: t.numel())
+    grads = [tuple(torch.empty_like(t) for t in c[2]) for c in cases]
+    for profiled in (False, True):      # events between the kernels keep them apart
+        F.profile_enable(profiled)
+        try:
+            seen = []
+            for _ in range(6):
+                for (win, args, _), g in zip(cases, grads):
+                    F.window_bwd(win, *args, ws, grads=g)
+                    seen.append([t.clone() for t in g])
+                    F.window_fwd(win, *args[:3], ws)
+                    for t in g:
+                        t.zero_()
+            torch.cuda.synchronize()
+        finally:
+            F.profile_enable(False)
+            F.profile_read()
+        assert F.device_status(ws) == 0
+        for n, got in enumerate(seen):
+            for a, b in zip(got, cases[n % len(cases)][2]):
+                assert torch.equal(a, b)
