@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(32 * W) norm_reduce_kernel(const NormArgs a, f
 }
 
 // ------------------------------------------------------------- wide rows
-// Sums of up to three values over the block.
+// Sums of two values over the block.
 __device__ inline void block_sum2(float& a, float& b, float (*red)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   a = warp_sum(a);
@@ -611,7 +611,7 @@ __device__ inline void from_f(float v, float* p) { *p = v; }
 __device__ inline void from_f(float v, __nv_bfloat16* p) { *p = __float2bfloat16(v); }
 
 template <typename T>
-__global__ void __launch_bounds__(WIDE) norm_fwd_wide_kernel(const NormArgs a, const T* __restrict__ x, T* __restrict__ y) {
+__global__ void __launch_bounds__(WIDE) norm_fwd_wide_kernel(const NormArgs a, const T* x, T* y) {   // y may be x
   __shared__ float red[2][32];
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* xr = x + r * a.x_stride;
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(WIDE) norm_fwd_wide_kernel(const NormArgs a, c
 
 template <typename T>
 __global__ void __launch_bounds__(WIDE)
-    norm_bwd_wide_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ dy, T* __restrict__ dx) {
+    norm_bwd_wide_kernel(const NormArgs a, const T* x, const T* dy, T* dx) {   // dx may be x or dy
   __shared__ float red[2][32];
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* xr = x + r * a.x_stride;
