@@ -437,6 +437,17 @@ __device__ inline bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile i
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// mbar_wait by every lane of a converged warp that goes on either way: where
+// the wait gave up, the numbers that follow are of no use (the status word
+// says so), and the warp leaves at its next wait that returns a result.  For
+// waits inside an item: agreeing on the result of each took 205 us where this
+// takes 199 (windowed attention, 2 x 32 heads, 4,099 tokens, window 1,024).
+__device__ inline void mbar_wait_step(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                      long long cap) {
+  mbar_wait(bar, parity, abort, status, cap);
+  __syncwarp();
+}
+
 // Wait that ignores `abort`: used on the way out to let copies or MMAs that
 // were already issued land before the block exits or frees TMEM.
 __device__ inline bool mbar_drain(uint64_t* bar, uint32_t parity, int* status, long long cap) {

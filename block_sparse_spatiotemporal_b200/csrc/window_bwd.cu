@@ -468,8 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     long long c = 0;
     int k = 0;
     uint32_t meets = 0;
-    bool ok = true;
-    for (int m = 0; ok; ++m) {
+    for (int m = 0;; ++m) {
       const int ib = m % ITEMS;
       if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(m / ITEMS) & 1, abort_flag, a.status, cap)) break;
       const Item<KV> it = ctl->item[ib];
@@ -500,10 +499,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int j = it.j0; j < it.j1; ++j, ++c) {
         const int b = (int)(c % NB), st = (int)(c % MST);
-        if (!mbar_wait_warp(&ctl->s_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap)) {
-          ok = false;
-          break;
-        }
+        mbar_wait_step(&ctl->s_full[b], (uint32_t)(c / NB) & 1, abort_flag, a.status, cap);
         tc_fence_after();
         const int m0 = it.moving(j) + 32 * part;  // this warp's columns
         const uint32_t mask = bits(sp.lo - m0, sp.hi - m0) | (KV ? 0u : bits(0, sp.sk - m0));
@@ -570,10 +566,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         mbar_arrive_warp(&ctl->p_full[b]);
       }
-      if (!ok) break;
       // ---- epilogue: accumulators to bf16 rows, or to this part's place in the workspace
       if (steps) {
-        if (!mbar_wait_warp(&ctl->acc_full, (uint32_t)k & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->acc_full, (uint32_t)k & 1, abort_flag, a.status, cap);
         ++k;
         tc_fence_after();
       }
@@ -620,10 +615,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the last of the tile's parts to arrive adds them in ascending order
         __threadfence();
         mbar_arrive_warp(&ctl->meet);
-        if (!mbar_wait_warp(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->meet, meets++ & 1, abort_flag, a.status, cap);
         if (threadIdx.x == CW0 * 32) ctl->last = atomicAdd(a.counters + it.cell, 1) == it.parts - 1;
         mbar_arrive_warp(&ctl->meet);
-        if (!mbar_wait_warp(&ctl->meet, meets++ & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->meet, meets++ & 1, abort_flag, a.status, cap);
         if (ctl->last) {
           __threadfence();
           const float* src = a.part + (long long)(idx - it.part) * 2 * 128 * D;

@@ -788,8 +788,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t chunks = ((1u << (4 / copies)) - 1u) << (copy * (4 / copies));
     uint32_t cnt = 0, meets = 0;
     int items = 0;
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
+    for (int n = 0;; ++n) {
       const int ib = n % ITEMS;
       if (!mbar_wait_warp(&ctl->item_full[ib], (uint32_t)(n / ITEMS) & 1, abort_flag, a.status, cap)) break;
       const Item& si = ctl->item[ib];
@@ -813,10 +812,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = j0; j < j1; ++j) {
         const int kt = j < ns ? j : t_lo + j - ns;
         if (!turn.on(j, kt)) continue;
-        if (!mbar_wait_warp(&ctl->s_full[t], cnt & 1, abort_flag, a.status, cap)) {
-          ok = false;
-          break;
-        }
+        mbar_wait_step(&ctl->s_full[t], cnt & 1, abort_flag, a.status, cap);
         tc_fence_after();
         any = true;
         if (warp_on) {
@@ -912,10 +908,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_arrive_warp(&ctl->p_full[t]);
         ++cnt;
       }
-      if (!ok) break;
       // ---- epilogue
       if (any) {
-        if (!mbar_wait_warp(&ctl->o_full[t], (uint32_t)items & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->o_full[t], (uint32_t)items & 1, abort_flag, a.status, cap);
         tc_fence_after();
         ++items;
       }
@@ -987,12 +982,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the group that completes the query tile's parts joins them
         __threadfence();
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
         const int base = idx - split;                  // split 0 of this item
         if (r == 0)
           ctl->last[t] = atomicAdd(a.counters + (DUAL ? base / a.splits * 2 + t : base / a.splits), 1) == a.parts / copies - 1;
         mbar_arrive_warp(&ctl->group[t]);
-        if (!mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap)) break;
+        mbar_wait_step(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
         if (ctl->last[t]) {
           __threadfence();
           const int left = seq.ql - tok0;
@@ -1003,20 +998,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           const JoinRows<128> jr{a.part_lse + row0, a.part_o + row0 * D, step, a.parts, rows};
           float* share = reinterpret_cast<float*>(sOut + t * 4 * OUT_STAGE);        // [batch of rows][parts]
           const int most = (int)(4 * OUT_STAGE / sizeof(float)) / a.parts;
-          bool joined = true;
-          for (int rb = 0; rb < rows && joined; rb += most) {
+          for (int rb = 0; rb < rows; rb += most) {
             const int re = rb + most < rows ? rb + most : rows;
             jr.load_lse(share, rb, re, r);
             mbar_arrive_warp(&ctl->group[t]);
-            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
-            if (!joined) break;
+            mbar_wait_step(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
             const int row = rb + r;
             if (row < re)
               a.lse[((long long)batch * g.H + head0 + row % a.pack) * g.Nq + tok0 + row / a.pack] =
                   jr.shares(share + r * a.parts);
             mbar_arrive_warp(&ctl->group[t]);
-            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
-            if (!joined) break;
+            mbar_wait_step(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
             jr.template sum<D>(share, rb, re, r, [&](int rr, int d0, const float (&v)[4]) {
               __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)batch * a.o_batch +
                                    (long long)(head0 + rr % a.pack) * a.o_head +
@@ -1024,9 +1016,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
             });
             mbar_arrive_warp(&ctl->group[t]);          // the shares are read
-            joined = mbar_wait_warp(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
+            mbar_wait_step(&ctl->group[t], meets++ & 1, abort_flag, a.status, cap);
           }
-          if (!joined) break;
         }
       }
     }
