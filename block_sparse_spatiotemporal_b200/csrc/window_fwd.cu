@@ -876,7 +876,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const float alpha = ex2(m_use - m_new);
                   if (over) m = m_new;
                   m_use = m_new;
-                  // (S waited for the PV of the group's step before, so O holds it)
+                  // (S waited for the PV of the group's step before, so O holds it).
+                  // What this step stored of P and, at an earlier move, of O is
+                  // read back here: loads wait only for stores that were waited for.
+                  tmem_wait_st();
                   scale_o<D>(tO, alpha);
                   l *= alpha;
 #pragma unroll 1
