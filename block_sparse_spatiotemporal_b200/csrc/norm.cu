@@ -16,10 +16,16 @@
 // 103 with gain and bias left out; vectors of 8, which read every other 16
 // bytes of the gain, took 149.  Where so few rows come that the SMs hold them
 // all at once, a row is spread thin (8 a thread) for the latency.
-// The variance never subtracts large sums: a row is shifted by its first
-// element, each thread takes the mean and the squared differences of its own
-// elements, and the parts are joined by
-// M2 = sum M2_i + sum n_i (mean_i - mean)^2, with one barrier a row.
+// The variance never subtracts large sums, and no rounding is larger than one
+// of the row's mean |x|: a warp takes the mean of its own elements as its
+// shift, and what the shift's rounding left (s) and M2 from the differences,
+//   shift = sum x / n, s = sum (x - shift) / n, M2 = sum (x - shift)^2 - n s^2;
+// with one barrier a row the warps are joined about A = sum n_i shift_i / C,
+//   e_i = (shift_i - A) + s_i, dm = sum n_i e_i / C, mean = A + dm,
+//   M2 = sum (M2_i + n_i e_i^2) - C dm^2,
+// and y comes from (x - A) - dm, which keeps what an fp32 mean cannot hold.  (A shift by the row's first element, as here
+// before, rounds every difference at that element's size: 8,192 wide with
+// x[0] = 1e4 among values near 1 it cost y 2e-4 and the mean 5e-4 of itself.)
 //
 // Backward: the column sums stay in the registers of a thread, which keeps
 // its columns (and their gain) for all its rows.  Blocks walk contiguous row
@@ -290,8 +296,7 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
     norm_fwd_kernel(const NormArgs a, const T* x, T* y) {
   using Ch = Chunks<T, VEC, EPT, FULL>;
   constexpr int N = Ch::N, NP = Ch::NP;
-  __shared__ float2 red[RW][MAX_WARPS];
-  __shared__ float red_n[MAX_WARPS];
+  __shared__ float4 red[RW][MAX_WARPS];        // a warp's shift, its residual mean, its M2, its elements
   const Lane L(a.warps);
   const Ch ch{{(L.t >> 5) * (32 * EPT / VEC) + L.lane, a.C / VEC}};
   const unsigned per_group = (unsigned)((a.rows_per_group + RW - 1) / RW);
@@ -307,84 +312,100 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
   bool on[RW];
 #pragma unroll
   for (int k = 0; k < RW; ++k) on[k] = in_group + k < a.rows_per_group;
-  uint64_t d[RW][N * NP];            // x - x0
-  float x0[RW], s[RW], m2[RW], m_t[RW];
+  uint64_t d[RW][N * NP];            // x
+  float A[RW], dm[RW], m2[RW];       // mean = A + dm, and M2 about it
   {
     typename Ch::Part raw[RW][N];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const T* row = x + (on[k] ? r0 + k : r0) * a.x_stride;
-      x0[k] = to_f(row[0]);
 #pragma unroll
       for (int c = 0; c < N; ++c)
         ch.load(row, c, raw[k][c]);
     }
-    const float n_t = ch.count(), inv_t = FULL ? 1.f / EPT : n_t > 0.f ? 1.f / n_t : 0.f;
-    const float n_w = FULL ? 32.f * EPT : warp_sum(n_t), inv_w = FULL ? 1.f / (32 * EPT) : n_w > 0.f ? 1.f / n_w : 0.f;
-    if (L.lane == 0) red_n[L.warp] = n_w;
+    const float n_w = FULL ? 32.f * EPT : warp_sum(ch.count()), inv_w = FULL ? 1.f / (32 * EPT) : 1.f / n_w;
+    // sum of the warp's elements over their number (scaled first: no sum overflows)
+    float shift[RW], s[RW];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      uint64_t s2[2] = {0ull, 0ull}, q2[2] = {0ull, 0ull};
-      const uint64_t X0 = both(x0[k]);
+      uint64_t s2[2] = {0ull, 0ull};
+      const uint64_t I = both(inv_w);
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         uint64_t p[NP];
         ch.pairs(raw[k][c], p);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          d[k][c * NP + i] = sub2(p[i], X0) & ch.mask(c);
-          s2[i & 1] = add2(s2[i & 1], d[k][c * NP + i]);
+          d[k][c * NP + i] = p[i] & ch.mask(c);
+          s2[i & 1] = fma2(d[k][c * NP + i], I, s2[i & 1]);
         }
       }
-      s[k] = sum2(add2(s2[0], s2[1]));
-      m_t[k] = s[k] * inv_t;
-      const uint64_t M = both(m_t[k]);
+      shift[k] = sum2(add2(s2[0], s2[1]));
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) shift[k] = warp_sum(shift[k]);
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      uint64_t s2[2] = {0ull, 0ull}, q2[2] = {0ull, 0ull};
+      const uint64_t S = both(shift[k]);
 #pragma unroll
       for (int c = 0; c < N; ++c) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const uint64_t e = sub2(d[k][c * NP + i], M) & ch.mask(c);
+          const uint64_t e = sub2(d[k][c * NP + i], S) & ch.mask(c);
+          s2[i & 1] = add2(s2[i & 1], e);
           q2[i & 1] = fma2(e, e, q2[i & 1]);
         }
       }
+      s[k] = sum2(add2(s2[0], s2[1]));
       m2[k] = sum2(add2(q2[0], q2[1]));
     }
 #pragma unroll
-    for (int k = 0; k < RW; ++k) s[k] = warp_sum(s[k]);
-#pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const float dw = m_t[k] - s[k] * inv_w;
-      m2[k] = warp_sum(fmaf(n_t * dw, dw, m2[k]));
+      s[k] = warp_sum(s[k]) * inv_w;             // what the shift's rounding left of the warp's mean
+      m2[k] = warp_sum(m2[k]);
+      m2[k] = fmaf(-n_w * s[k], s[k], m2[k]);
     }
     if (L.warps > 1) {
       if (L.lane == 0) {
 #pragma unroll
-        for (int k = 0; k < RW; ++k) red[k][L.warp] = make_float2(s[k] * inv_w, m2[k]);
+        for (int k = 0; k < RW; ++k) red[k][L.warp] = make_float4(shift[k], s[k], m2[k], n_w);
       }
       team_sync(L.warps, L.id);
-      const float2(*rd)[MAX_WARPS] = red;
+      const float4(*rd)[MAX_WARPS] = red;
 #pragma unroll
-      for (int k = 0; k < RW; ++k) s[k] = m2[k] = 0.f;
+      for (int k = 0; k < RW; ++k) A[k] = dm[k] = m2[k] = 0.f;
       for (int i = L.id * L.warps; i < (L.id + 1) * L.warps; ++i)
 #pragma unroll
-        for (int k = 0; k < RW; ++k) s[k] = fmaf(FULL ? 32.f * EPT : red_n[i], rd[k][i].x, s[k]);
+        for (int k = 0; k < RW; ++k) A[k] = fmaf(rd[k][i].w * inv_c, rd[k][i].x, A[k]);
       for (int i = L.id * L.warps; i < (L.id + 1) * L.warps; ++i)
 #pragma unroll
         for (int k = 0; k < RW; ++k) {
-          const float dm = rd[k][i].x - s[k] * inv_c;
-          m2[k] += fmaf((FULL ? 32.f * EPT : red_n[i]) * dm, dm, rd[k][i].y);
+          const float4 w = rd[k][i];
+          const float e = (w.x - A[k]) + w.y;    // the warp's mean from A
+          dm[k] = fmaf(w.w * inv_c, e, dm[k]);
+          m2[k] += fmaf(w.w * e, e, w.z);
         }
+#pragma unroll
+      for (int k = 0; k < RW; ++k) m2[k] = fmaf(-(float)a.C * dm[k], dm[k], m2[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        A[k] = shift[k];
+        dm[k] = s[k];
+      }
     }
   }
-  uint64_t RS[RW], MR[RW];
+  uint64_t RS[RW], MA[RW], MR[RW];
 #pragma unroll
   for (int k = 0; k < RW; ++k) {
-    const float mean = s[k] * inv_c;             // of x - x0
-    const float rstd = rsqrt_near(fmaf(m2[k], inv_c, a.eps));
+    const float var = m2[k] < 0.f ? 0.f : m2[k] * inv_c;       // (NaN stays)
+    const float rstd = rsqrt_near(var + a.eps);
     RS[k] = both(rstd);
-    MR[k] = both(sizeof(T) == 4 ? -mean : -mean * rstd);
+    MA[k] = both(A[k]);
+    MR[k] = both(sizeof(T) == 4 ? -dm[k] : -dm[k] * rstd);
     if (L.t == 0 && on[k]) {
-      if (a.mean_out) a.mean_out[r0 + k] = x0[k] + mean;
+      if (a.mean_out) a.mean_out[r0 + k] = dm[k] == dm[k] ? A[k] + dm[k] : A[k];   // an infinity is the mean's own
       if (a.rstd_out) a.rstd_out[r0 + k] = rstd;
     }
   }
@@ -398,8 +419,8 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
     for (int k = 0; k < RW; ++k) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const uint64_t e = d[k][c * NP + i];
-        // fp32 keeps the difference exact to its own rounding; a bf16 output does not need the operation
+        const uint64_t e = sub2(d[k][c * NP + i], MA[k]);
+        // fp32: the difference rounded at its own size; a bf16 output does not need the operation
         const uint64_t xh = sizeof(T) == 4 ? mul2(add2(e, MR[k]), RS[k]) : fma2(e, RS[k], MR[k]);
         o[i] = fma2(xh, w[i], b[i]);
       }

@@ -1,0 +1,41 @@
+"""GPU parity of the layer norm on rows that are hard on its arithmetic:
+one element far from the others, against the bounds of the other norm tests
+(every rounding is one of the row's mean |x|, wherever the far element is)."""
+import pytest
+import torch
+
+from block_sparse_spatiotemporal_b200 import fvattn as F
+from tests.test_gpu_norm import DT, check_bwd, check_fwd, make, plain
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("far", [1e2, 1e4])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("rows,C", [(3, 64), (700, 64), (5, 1000), (2000, 1001), (4, 1024), (3, 5120), (600, 5120),
+                                    (6, 8192), (700, 8192), (3, 10000)])
+def test_one_far_element(rows, C, where, far, dtype):
+    x, w, b, dy = make(rows, C, 1, dtype, 7)
+    x = (x.float().clamp(-1, 1) + 1).to(DT[dtype][0])
+    x[:, {"first": 0, "middle": C // 2, "last": C - 1}[where]] = far
+    norm = F.make_norm(rows, C, 1, dtype=DT[dtype][1])
+    y, mean, rstd = F.layer_norm_fwd(norm, x, weight=w, bias=b)
+    r = plain(x, w, b, dy, 1, 1e-6, False)
+    check_fwd(y, mean, rstd, r, x, DT[dtype][2])
+    check_bwd(*F.layer_norm_bwd(norm, x, dy, mean, rstd, F.norm_workspace(norm), weight=w), r, DT[dtype][2])
+
+
+def test_the_mean_of_rows_with_an_infinity():
+    """An infinite element makes the row's mean infinite and its y NaN; a NaN
+    makes both NaN; the other rows stay as they are."""
+    for rows, C in ((4, 64), (4, 3000), (900, 3000)):
+        x = torch.randn(rows, C, generator=torch.Generator("cuda").manual_seed(0), device="cuda")
+        norm = F.make_norm(rows, C, dtype=F.F32)
+        y0, mean0, rstd0 = F.layer_norm_fwd(norm, x)
+        x[1, C - 1], x[2, 0], x[3, C // 2] = float("inf"), -float("inf"), float("nan")
+        y, mean, rstd = F.layer_norm_fwd(norm, x)
+        assert mean[1] == float("inf") and mean[2] == -float("inf") and mean[3].isnan()
+        assert y[1:4].isnan().all() and rstd[1:4].isnan().all()
+        for i in (0, *range(4, rows, 100)):
+            assert torch.equal(y[i], y0[i]) and mean[i] == mean0[i] and rstd[i] == rstd0[i]
