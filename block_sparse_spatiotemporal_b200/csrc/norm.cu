@@ -431,8 +431,10 @@ __global__ void __launch_bounds__(EPT == 8 ? 1024 : EPT == 16 ? 512 : 256, EPT =
 
 // dx of the block's rows and the block's column sums per group.  The second
 // pass over a row reads the ring again: the sums take the registers.  There
-// dx = rstd gy + x A + B with A = -rstd^2 c2, B = rstd^2 c2 mean - rstd c1
-// (c1, c2 the two row means), whose rounding is that of the saved mean.
+// dx = rstd gy + (x - mean) A + B with A = -rstd^2 c2, B = -rstd c1 (c1, c2
+// the two row means).  The mean is taken off before anything is scaled: with
+// mean rstd in a product of its own, its rounding, 2^-24 |mean| rstd, stays in
+// every xhat.
 template <typename T, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
     norm_bwd_kernel(const NormArgs a, const T* x, const T* dy, T* dx) {
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
       }
       if constexpr (!Rg::WORDS) copy_wait<STAGES - 1>();
       uint64_t C1 = 0ull, C2 = 0ull;
-      const uint64_t RS = both(rstd), MR = both(-mean * rstd);
+      const uint64_t RS = both(rstd), MN = both(mean);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
           uint64_t xv[NP], gv[NP];
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             gv[i] &= ch.mask(k);                    // an absent element adds nothing
-            const uint64_t xh = fma2(xv[i], RS, MR);
+            const uint64_t xh = mul2(sub2(xv[i], MN), RS);
             aw[k * NP + i] = fma2(gv[i], xh, aw[k * NP + i]);
             ab[k * NP + i] = add2(ab[k * NP + i], gv[i]);
             const uint64_t gy = mul2(gv[i], w[k][i]);
@@ -525,8 +527,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
           c2 = warp_sum(p.y);
           par ^= 1;
         }
-        const float A = -rstd * rstd * (c2 * inv_c);
-        const uint64_t KA = both(A), KB = both(fmaf(-A, mean, -rstd * (c1 * inv_c)));
+        const uint64_t KA = both(-rstd * rstd * (c2 * inv_c)), KB = both(-rstd * (c1 * inv_c));
         T* dr = dx + r * a.x_stride;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
             ch.get(rx, st, k, xr, xv);
             ch.get(ry, st, k, yr, gv);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) xv[i] = fma2(mul2(gv[i], w[k][i]), RS, fma2(xv[i], KA, KB));
+            for (int i = 0; i < NP; ++i) xv[i] = fma2(mul2(gv[i], w[k][i]), RS, fma2(sub2(xv[i], MN), KA, KB));
             ch.put(dr, k, xv);
           }
       }

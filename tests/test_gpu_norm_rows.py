@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from block_sparse_spatiotemporal_b200 import fvattn as F
-from tests.test_gpu_norm import DT, check_bwd, check_fwd, make, plain
+from tests.test_gpu_norm import DT, check_bwd, check_fwd, make, plain, within
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,39 @@ def test_the_mean_of_rows_with_an_infinity():
         assert y[1:4].isnan().all() and rstd[1:4].isnan().all()
         for i in (0, *range(4, rows, 100)):
             assert torch.equal(y[i], y0[i]) and mean[i] == mean0[i] and rstd[i] == rstd0[i]
+
+
+def by_the_saved_statistics(x, dy, gain, mean, rstd, groups):
+    """(dx, dw, their error scales) of the backward's formula in 64 bits, for the statistics it is given."""
+    x, dy, mean, rstd = x.double(), dy.double(), mean.double()[:, None], rstd.double()[:, None]
+    gain = gain.double().repeat_interleave(x.shape[0] // groups, 0)
+    xh, gy = (x - mean) * rstd, dy * gain
+    dx = rstd * (gy - gy.mean(1, keepdim=True) - xh * (gy * xh).mean(1, keepdim=True))
+    size = rstd * (gy.abs() + gy.abs().mean(1, keepdim=True) + xh.abs() * (gy * xh).abs().mean(1, keepdim=True))
+    cols = lambda t: t.reshape(groups, -1, t.shape[1]).sum(1)  # noqa: E731
+    return dx, cols(dy * xh), size, cols((dy * xh).abs())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C,groups", [(40, 64, 2), (300, 1001, 3), (150, 1536, 1), (60, 5120, 4), (8, 9000, 2)])
+def test_backward_with_a_mean_far_above_the_deviation(rows, C, groups, dtype):
+    """mean / std of 600 (three of 64 elements a step above the others:
+    2^7 / sqrt(3/64 61/64)) to 12,000: x - mean is off by 2^-24 of itself, so dx and
+    dweight keep the bounds of ordinary rows, 2^-18 and 2^-17 of their terms'
+    magnitudes, for the statistics they are given."""
+    gen = torch.Generator("cuda").manual_seed(12)
+    if dtype == "f32":
+        x = torch.randn(rows, C, generator=gen, device="cuda") + 4096.0
+    else:                            # a few elements one bf16 step above the others
+        x = torch.where(torch.rand(rows, C, generator=gen, device="cuda") < 2.0 ** -10, 1 + 2.0 ** -7, 1.0)
+        x[:, 5] = 1 + 2.0 ** -7
+        x = x.to(torch.bfloat16)
+    dy = torch.randn(rows, C, generator=gen, device="cuda").to(DT[dtype][0])
+    w = torch.randn(groups, C, generator=gen, device="cuda")
+    norm = F.make_norm(rows, C, groups, dtype=DT[dtype][1], eps=0.0)
+    _, mean, rstd = F.layer_norm_fwd(norm, x, weight=w)
+    assert float((mean.abs() * rstd).min()) > 600
+    dx, dw, db = F.layer_norm_bwd(norm, x, dy, mean, rstd, F.norm_workspace(norm), weight=w)
+    want_dx, want_dw, size, aw = by_the_saved_statistics(x, dy, w, mean, rstd, groups)
+    within(dx, want_dx, DT[dtype][2] * want_dx.abs() + 2.0 ** -18 * size, "dx")
+    within(dw, want_dw, 2.0 ** -17 * aw, "dweight")
