@@ -105,10 +105,11 @@ __device__ inline void team_sync(int warps, int id) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(32 * warps) : "memory");
 }
 
-// 1 / sqrt(v): the approximation (2 steps of fp32 at most) and one Newton step.
+// 1 / sqrt(v): the approximation (2 steps of fp32 at most) and one Newton step
+// (v r first: half of a variance below 2^-126 would lose its last bits).
 __device__ inline float rsqrt_near(float v) {
   const float r = rsqrtf(v);
-  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+  return v > 0.f && v < INFINITY ? r * fmaf(-0.5f * (v * r), r, 1.5f) : r;
 }
 
 struct Range {

@@ -75,3 +75,18 @@ def test_backward_with_a_mean_far_above_the_deviation(rows, C, groups, dtype):
     want_dx, want_dw, size, aw = by_the_saved_statistics(x, dy, w, mean, rstd, groups)
     within(dx, want_dx, DT[dtype][2] * want_dx.abs() + 2.0 ** -18 * size, "dx")
     within(dw, want_dw, 2.0 ** -17 * aw, "dweight")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C", [(3, 256), (2000, 256), (3, 1024), (900, 1024), (900, 8192), (3, 16384)])
+def test_a_variance_of_three_smallest_steps(rows, C, dtype):
+    """eps = 0 and three of eight elements +-2^-73, the others 0: every sum is
+    exact, the variance is 3 x 2^-149, and rstd and y are it to 2^-21 (the
+    root's 2^-22, a product's 2^-24; bf16: half a step of y)."""
+    a = 2.0 ** -73
+    x = torch.tensor([a, -a, a, -a, a, -a] + [0.0] * 10, device="cuda").repeat(rows, C // 16).to(DT[dtype][0])
+    y, mean, rstd = F.layer_norm_fwd(F.make_norm(rows, C, dtype=DT[dtype][1], eps=0.0), x)
+    want = (3 * 2.0 ** -149) ** -0.5
+    assert (mean == 0).all()
+    assert ((rstd.double() - want).abs() <= 2.0 ** -21 * want).all()
+    within(y, x.double() * want, (DT[dtype][2] + 2.0 ** -21) * (x.double() * want).abs(), "y")
