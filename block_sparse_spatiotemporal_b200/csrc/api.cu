@@ -1472,6 +1472,11 @@ int fvattn_profile_enable(int enable) {
 }
 
 int fvattn_profile_read(double* ms, int64_t* launches) {
+  return fvattn_profile_read_stages(ms, launches, FVATTN_STAGE_READ);
+}
+
+int fvattn_profile_read_stages(double* ms, int64_t* launches, int32_t count) {
+  if (count < 0) return FVATTN_ERR_INVALID_ARG;
   Profiler& p = prof();
   std::lock_guard<std::mutex> lock(p.mu);
   double acc[FVATTN_STAGE_COUNT] = {0};
@@ -1487,9 +1492,9 @@ int fvattn_profile_read(double* ms, int64_t* launches) {
     p.pool.push_back(r.b);
   }
   p.recs.clear();
-  for (int i = 0; i < FVATTN_STAGE_COUNT; ++i) {
-    if (ms) ms[i] = acc[i];
-    if (launches) launches[i] = cnt[i];
+  for (int32_t i = 0; i < count; ++i) {
+    if (ms) ms[i] = i < FVATTN_STAGE_COUNT ? acc[i] : 0.0;
+    if (launches) launches[i] = i < FVATTN_STAGE_COUNT ? cnt[i] : 0;
   }
   return st;
 }

@@ -156,6 +156,7 @@ _SIGS = {
     "fvattn_selftest_wait_timeout": [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_void_p],
     "fvattn_profile_enable": [ctypes.c_int],
     "fvattn_profile_read": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)],
+    "fvattn_profile_read_stages": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), ctypes.c_int32],
     "fvattn_status_string": [ctypes.c_int],
 }
 
@@ -697,5 +698,5 @@ def profile_read():
     """{stage: (ms, launches)} summed since the last read (synchronises)."""
     ms = (ctypes.c_double * len(STAGES))()
     n = (ctypes.c_int64 * len(STAGES))()
-    _check("fvattn_profile_read", lib().fvattn_profile_read(ms, n))
+    _check("fvattn_profile_read_stages", lib().fvattn_profile_read_stages(ms, n, len(STAGES)))
     return {name: (ms[i], n[i]) for i, name in enumerate(STAGES)}

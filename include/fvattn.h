@@ -446,11 +446,14 @@ int fvattn_selftest_wait_timeout(void* ws, size_t ws_bytes, int64_t cap_iteratio
 
 /* Per-stage timing.  While enabled, every entry point records a pair of CUDA
  * events on its stream around each stage it runs (host-side event objects
- * only; no device memory).  fvattn_profile_read synchronises on the recorded
- * events, writes per stage the summed milliseconds and the number of this
- * library's kernels launched into ms[FVATTN_STAGE_COUNT] and
- * launches[FVATTN_STAGE_COUNT] (either may be NULL) and clears the record.  Not thread-safe against
- * concurrent calls from several host threads. */
+ * only; no device memory).  fvattn_profile_read_stages synchronises on the
+ * recorded events, writes per stage the summed milliseconds and the number of
+ * this library's kernels launched into ms[count] and launches[count] (either
+ * may be NULL; entries past the last stage are 0) and clears the record.
+ * fvattn_profile_read is the same for the first FVATTN_STAGE_READ stages, the
+ * ones there were when it came, and never writes more, however many stages
+ * are added: its callers have no other way to say how long their arrays are.
+ * Not thread-safe against concurrent calls from several host threads. */
 typedef enum {
   FVATTN_STAGE_TABLES = 0,    /* tile / token / RoPE tables */
   FVATTN_STAGE_REORDER = 1,   /* fvattn_tile_reorder */
@@ -470,8 +473,10 @@ typedef enum {
   FVATTN_STAGE_WINDOW_Q = 15,    /* its backward: query-stationary dQ kernel */
   FVATTN_STAGE_COUNT = 16
 } fvattn_stage;
+#define FVATTN_STAGE_READ 10
 int fvattn_profile_enable(int enable);
 int fvattn_profile_read(double* ms, int64_t* launches);
+int fvattn_profile_read_stages(double* ms, int64_t* launches, int32_t count);
 
 /* Per-CTA busy time of the persistent fine stage, the single-GPU analogue of
  * the per-rank load the "FVAttn" digest balances (section 02; section 03
