@@ -500,7 +500,8 @@ def norm_workspace(norm: Norm, device="cuda") -> torch.Tensor:
 
 
 def _rows(t: torch.Tensor, norm: Norm, stride: int, what: str):
-    """Pointer of the rows of t: contiguous [..., channels], or [rows, channels] with norm's row stride."""
+    """Pointer of the rows of t: contiguous [..., channels], or [rows, channels] with norm's row stride,
+    16-byte aligned."""
     C, rows = norm.channels, norm.rows
     stride = stride or C
     ok = t.dtype is _DTYPES.get(norm.dtype) and t.dim() >= 1 and t.shape[-1] == C and t.numel() == rows * C
@@ -510,7 +511,10 @@ def _rows(t: torch.Tensor, norm: Norm, stride: int, what: str):
         ok = t.dim() == 2 and (t.stride(1) == 1 or C == 1) and (rows == 1 or t.stride(0) == stride)
     if not ok:
         raise ValueError(f"{what}: expected {rows} {_DTYPES.get(norm.dtype)} rows of {C} with row stride {stride}")
-    return t.data_ptr()
+    p = t.data_ptr()
+    if p & 15 and rows:
+        raise ValueError(f"{what}: the rows have to start on a 16-byte boundary")
+    return p
 
 
 def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
@@ -522,8 +526,8 @@ def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
 
 
 def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rstd=None, stream=None):
-    """Layer norm of the rows of x ([..., channels]) with weight and bias
-    [groups, channels] float32 (or None): returns (y, mean, rstd)."""
+    """Layer norm of the rows of x ([..., channels], starting on 16 bytes) with
+    weight and bias [groups, channels] float32 (or None): returns (y, mean, rstd)."""
     affine, per_row = (norm.groups, norm.channels), (norm.rows,)
     s, guards = _enter((x, weight, bias, y, mean, rstd), stream)
     try:

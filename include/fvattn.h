@@ -337,9 +337,9 @@ int fvattn_qkv_rope(const fvattn_shape* shape, const void* x, int32_t channels, 
  * per sample or per latent frame).
  *   x, y, dy, dx: `rows` rows of `channels` values, float32 or bf16 (dtype);
  *     row r of x and dx starts x_stride elements after row r - 1, of y and dy
- *     y_stride (0 = channels; at least channels).  Any element alignment of
- *     the rows is taken; strides and channels that are multiples of 16 bytes
- *     are the fast ones.
+ *     y_stride (0 = channels; at least channels).  The tensors start on 16
+ *     bytes; strides and channels may be any number of elements, multiples of
+ *     16 bytes are the fast ones.
  *   weight, bias: [groups, channels] float32, either may be NULL (1 and 0).
  *     Row r belongs to group r / (rows / groups); its gain is weight, or
  *     1 + weight with gain_one != 0.
