@@ -517,6 +517,13 @@ def _rows(t: torch.Tensor, norm: Norm, stride: int, what: str):
     return p
 
 
+def _affine(t: Optional[torch.Tensor], norm: Norm, what: str):
+    """Pointer of a weight, bias or gradient of one: float32 [groups, channels],
+    or a single group's [channels]."""
+    one = norm.groups == 1 and t is not None and t.dim() == 1
+    return _typed(t, torch.float32, (norm.channels,) if one else (norm.groups, norm.channels), what)
+
+
 def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
     """An output like `like` with norm's row stride."""
     if stride in (0, norm.channels) or norm.rows <= 1:
@@ -527,8 +534,9 @@ def _new_rows(like: torch.Tensor, norm: Norm, stride: int):
 
 def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rstd=None, stream=None):
     """Layer norm of the rows of x ([..., channels], starting on 16 bytes) with
-    weight and bias [groups, channels] float32 (or None): returns (y, mean, rstd)."""
-    affine, per_row = (norm.groups, norm.channels), (norm.rows,)
+    weight and bias [groups, channels] float32 (a single group's may be
+    [channels]; or None): returns (y, mean, rstd)."""
+    per_row = (norm.rows,)
     s, guards = _enter((x, weight, bias, y, mean, rstd), stream)
     try:
         px = _rows(x, norm, norm.x_stride, "x")
@@ -544,8 +552,8 @@ def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rst
         elif rstd is None:
             rstd = torch.empty_like(mean)
         _check("fvattn_layer_norm_fwd",
-               lib().fvattn_layer_norm_fwd(ctypes.byref(norm), px, _typed(weight, torch.float32, affine, "weight"),
-                                           _typed(bias, torch.float32, affine, "bias"), py,
+               lib().fvattn_layer_norm_fwd(ctypes.byref(norm), px, _affine(weight, norm, "weight"),
+                                           _affine(bias, norm, "bias"), py,
                                            _typed(mean, torch.float32, per_row, "mean"),
                                            _typed(rstd, torch.float32, per_row, "rstd"), s))
     finally:
@@ -555,9 +563,10 @@ def layer_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, mean=None, rst
 
 
 def layer_norm_bwd(norm: Norm, x, dy, mean, rstd, ws, weight=None, grads=None, stream=None):
-    """Backward of layer_norm_fwd: returns (dx, dweight, dbias).  grads: the
-    three output tensors, None for a gradient that is not wanted."""
-    affine, per_row = (norm.groups, norm.channels), (norm.rows,)
+    """Backward of layer_norm_fwd: returns (dx, dweight, dbias), the last two
+    shaped like weight (without one: [groups, channels]).  grads: the three
+    output tensors, None for a gradient that is not wanted."""
+    affine, per_row = (norm.groups, norm.channels) if weight is None else weight.shape, (norm.rows,)
     s, guards = _enter((x, dy, mean, rstd, ws, weight, *(grads or ())), stream)
     try:
         px = _rows(x, norm, norm.x_stride, "x")
@@ -567,12 +576,12 @@ def layer_norm_bwd(norm: Norm, x, dy, mean, rstd, ws, weight=None, grads=None, s
         dx, dw, db = grads
         _check("fvattn_layer_norm_bwd",
                lib().fvattn_layer_norm_bwd(ctypes.byref(norm), px, _rows(dy, norm, norm.y_stride, "dy"),
-                                           _typed(weight, torch.float32, affine, "weight"),
+                                           _affine(weight, norm, "weight"),
                                            _typed(mean, torch.float32, per_row, "mean"),
                                            _typed(rstd, torch.float32, per_row, "rstd"),
                                            None if dx is None else _rows(dx, norm, norm.x_stride, "dx"),
-                                           _typed(dw, torch.float32, affine, "dweight"),
-                                           _typed(db, torch.float32, affine, "dbias"), _ptr(ws), ws.numel(), s))
+                                           _affine(dw, norm, "dweight"), _affine(db, norm, "dbias"),
+                                           _ptr(ws), ws.numel(), s))
     finally:
         if guards is not None:
             guards.close()
