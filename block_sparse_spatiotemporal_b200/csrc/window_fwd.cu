@@ -5,10 +5,10 @@
 // units before it, and the first `sinks` units (see span_of).
 //   s = scale q k^T, out = sum_j 2^(s'_j - m) v_j / sum_j 2^(s'_j - m),
 //   s' = s log2(e), lse = ln 2 (m + log2 sum_j 2^(s'_j - m)),
-// in one pass over the visible keys.  The reference m of a row is the largest
-// logit of its first visible key tile; it moves (and O is rescaled) only when
-// the probabilities of a later tile sum past 2^64, which fp32 sums and bf16
-// probabilities hold without loss, so no step takes a row maximum.
+// in one pass over the visible keys.  The reference m of a row stands 40 above
+// the largest logit of its first visible key tile; it moves (and O is rescaled)
+// only when the probabilities of a later tile sum past 2^24, which fp32 sums
+// and bf16 probabilities hold without loss, so no step takes a row maximum.
 //
 // Persistent kernel, one CTA per SM, 384 threads, over items of two 128-row
 // query tiles A, B that share one stream of 128-key tiles:
@@ -64,7 +64,16 @@ namespace win {
 constexpr int THREADS = 384;
 constexpr int SW0 = 4;                       // first softmax warp
 constexpr uint32_t PART = 128 * 128;         // 64 dims of 128 rows: 16 KB
-constexpr float RESCALE_SUM = 18446744073709551616.f;   // 2^64
+// A row's reference stands 2^HEAD above the largest logit it was taken from,
+// and a step's probabilities (of 128 keys; few queries: of 32) may sum to
+// RESCALE_SUM before it moves: logits may rise by 64 in base 2, so moves are
+// rare (without the head and with sums up to 2^24, logits of a spread of 10
+// took 316 us where this takes 212, at 2 x 32 heads, 4,099 tokens, window
+// 1,024), and O, sums of probabilities times V over up to 2^21 steps, stays in
+// fp32 for |v| up to 2^80 (at most 2^21 2^26 2^80) and down to 2^-80 (2^-40
+// 2^-80 and 2^-6 of it are normal numbers).
+constexpr float HEAD = 40.f, HEAD_MUL = 1099511627776.f;   // 2^40
+constexpr float RESCALE_SUM = 16777216.f;    // 2^24
 constexpr uint32_t TMEM_COLS = 512, TM_S = 0, TM_O = 256;
 
 constexpr int ITEMS = 2;                     // items published ahead
@@ -821,7 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if constexpr (DUAL) {
             if (unset) {                         // some row has met no visible key yet
               const float mx = max_row(tS, sp, key0) * sl2;
-              if (m == -INFINITY) m = mx;
+              if (m == -INFINITY) m = mx + HEAD;
               unset = __any_sync(0xffffffffu, m == -INFINITY);
             }
             uint32_t pk[64];
@@ -834,7 +843,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               // S), so O holds the earlier steps; before an item's first PV it
               // holds nothing that is used.
               const float mx = fmaxf(max_row(tS, sp, key0) * sl2, m_use);
-              const float m_new = over ? mx : m_use;
+              const float m_new = over ? mx + HEAD : m_use;
               const float alpha = ex2(m_use - m_new);
               if (over) m = m_new;
               sum = exp_row<true>(tS, sl2, m_new, sp, key0, pk);
@@ -854,7 +863,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int k0 = key0 + 32 * c;
                 if (unset) {
                   const float mx = max_chunk(tC, sp, k0) * sl2;
-                  if (m == -INFINITY) m = mx;
+                  if (m == -INFINITY) m = mx + HEAD;
                   unset = __any_sync(0xffffffffu, m == -INFINITY);
                 }
                 float m_use = m == -INFINITY ? 0.f : m;
@@ -872,7 +881,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   if (!__any_sync(0xffffffffu, over)) break;
                   // as above; what this step already holds of P moves too
                   const float mx = fmaxf(max_chunk(tC, sp, k0) * sl2, m_use);   // by every lane: TMEM loads are the warp's
-                  const float m_new = over ? mx : m_use;
+                  const float m_new = over ? mx + HEAD : m_use;
                   const float alpha = ex2(m_use - m_new);
                   if (over) m = m_new;
                   m_use = m_new;
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++items;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f || l != l ? m + __log2f(l) : -INFINITY;
+      const float lse2 = l > 0.f || l != l ? (m - HEAD) + __log2f(l * HEAD_MUL) : -INFINITY;
       const bool parts = !DUAL || a.parts > 1;
       const long long slot = parts ? (((long long)idx * 2 + t) * copies + copy) * prow + rl : 0;
       if (warp_on) {

@@ -392,6 +392,8 @@ int fvattn_layer_norm_bwd(const fvattn_norm* norm, const void* x, const void* dy
  *   between sinks and the first query's window) may hold anything, NaN
  *   included.  Visible k and v must be finite for the others to stay so: a
  *   NaN that only some queries of a sequence see can reach its other queries.
+ *   The sums on the way to out stay in fp32 for |v| from 2^-80 to 2^80; beyond
+ *   that they may overflow or lose bits.
  * Few queries (single tokens against a cache) split the keys over the GPU
  * and join the parts in a fixed order: every result is deterministic. */
 typedef struct {

@@ -46,3 +46,23 @@ def test_moves_that_leave_weight_behind(twice, rise, Nq, D):
     check_far(out, lse, plain_fwd(q, k, v, 1, 0, 0, scale=math.log(2.0)))
     again = run(win, q, k, v)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Nq,B", [(1, 1), (4, 150), (40, 150), (100, 150), (200, 40)])
+def test_large_and_small_values_under_a_reference_that_lags(Nq, B, D):
+    """|v| up to 2^80 and down to 2^-80 with most keys' logits far above the
+    first tile's, or at its level: the output is a mean of v, and no sum on the
+    way to it leaves fp32."""
+    H, Nk = 1, 2000
+    gen = torch.Generator("cuda").manual_seed(13)
+    q = torch.zeros(B, H, Nq, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    k = torch.randn(B, H, Nk, D, generator=gen, device="cuda").to(torch.bfloat16)
+    for rise, size in ((15, 79), (18, 79), (50, 79), (56, 79), (0, 79), (0, -80), (56, -80)):
+        k[..., 0] = (torch.arange(Nk, device="cuda") >= 140).to(torch.bfloat16) * rise
+        v = (torch.rand(B, H, Nk, D, generator=gen, device="cuda") + 1).to(torch.bfloat16) * 2.0 ** size
+        win = F.make_window(B, H, D, Nq, Nk, 0, scale=math.log(2.0))
+        out, lse = run(win, q, k, v)
+        assert out.isfinite().all()
+        check_far(out, lse, plain_fwd(q, k, v, 1, 0, 0, scale=math.log(2.0)))
