@@ -20,7 +20,7 @@
 // Per step two warps issue S = X0 Y0^T and dP = X1 Y1^T (X stationary: K, V
 // or Q, dO; Y moving) into one of NB TMEM buffers, eight warps (two per TMEM
 // lane quarter, half the columns each) turn them into P and dS and write both
-// back into the same columns as bf16 (rounded to 2^-9 relative: the operands
+// back into the same columns as bf16 (off by up to 2^-8 of it: the operands
 // of the next products), and a fourth warp's accumulating MMAs read them from
 // TMEM as the A operand.  The moving tiles are used twice: K-major for the
 // scores, MN-major for the accumulations.

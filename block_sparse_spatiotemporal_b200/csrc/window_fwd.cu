@@ -28,7 +28,7 @@
 //                exponentials, and a step took 5,260 clocks instead of 4,200;
 //   warps 4-7, 8-11   softmax of tile A, B: thread r owns row r; P is
 //                written back over S as bf16 (the A operand of the PV MMA;
-//                its rounding, relative 2^-9, is the step's largest error).
+//                its rounding, relative 2^-8, is the step's largest error).
 // Key tiles that none of a tile's rows sees are skipped for that tile, and
 // only tiles that some row sees in part are masked.  Output rows go through
 // shared memory so that a store writes whole 128-byte lines (a thread storing
