@@ -10,12 +10,14 @@
 //
 // Forward: a block takes two rows of one group at once and holds them in
 // registers, 32 elements a thread in vectors of 4: gain and bias are then one
-// fully coalesced 16-byte load a vector, shared by both rows.  They come from
-// L1, and there lies the limit next to the memory: at 33,280 x 5,120 bf16
-// (104 us of memory at a copy's rate) one row a block took 135 us, two 119,
-// 103 with gain and bias left out; vectors of 8, which read every other 16
-// bytes of the gain, took 149.  Where so few rows come that the SMs hold them
-// all at once, a row is spread thin (8 a thread) for the latency.
+// fully coalesced 16-byte load a vector, shared by both rows and coming from
+// L1.  At 33,280 x 5,120 bf16 (104 us of memory at a copy's rate) it takes 139
+// us, one row a block 201, 16 elements a thread 213, vectors of 8, which read
+// every other 16 bytes of the gain, 152.  Without gain and bias it takes 135:
+// what keeps it from the memory's rate is that an SM holds three blocks (128
+// registers a thread), which load, meet and store in turn; most stalls wait
+// for loads.  Where so few rows come that the SMs hold them all at once, a row
+// is spread thin (8 a thread) for the latency.
 // The variance never subtracts large sums, and no rounding is larger than one
 // of the row's mean |x|: a warp takes the mean of its own elements as its
 // shift, and what the shift's rounding left (s) and M2 from the differences,
@@ -23,9 +25,10 @@
 // with one barrier a row the warps are joined about A = sum n_i shift_i / C,
 //   e_i = (shift_i - A) + s_i, dm = sum n_i e_i / C, mean = A + dm,
 //   M2 = sum (M2_i + n_i e_i^2) - C dm^2,
-// and y comes from (x - A) - dm, which keeps what an fp32 mean cannot hold.  (A shift by the row's first element, as here
-// before, rounds every difference at that element's size: 8,192 wide with
-// x[0] = 1e4 among values near 1 it cost y 2e-4 and the mean 5e-4 of itself.)
+// and y comes from (x - A) - dm, which keeps what an fp32 mean cannot hold.
+// (A shift by the row's first element rounds every difference at that
+// element's size: 8,192 wide with x[0] = 1e4 among values near 1 it cost y
+// 2e-4 and the mean 5e-4 of itself.  Both take the same time within 1%.)
 //
 // Backward: the column sums stay in the registers of a thread, which keeps
 // its columns (and their gain) for all its rows.  Blocks walk contiguous row
@@ -283,7 +286,7 @@ template <typename T, int VEC, int EPT, bool FULL> struct Chunks {
 };
 
 // Warps of a backward block: 96 registers a thread with wide vectors (20 warps;
-// 15 of 32 elements a thread took 283 us where 20 of 16 take 195), 128 with
+// 15 of 32 elements a thread took 275 us where 20 of 16 take 210), 128 with
 // narrow ones, which spill below that.
 template <int VEC> __host__ __device__ constexpr int bwd_warps() { return VEC >= 4 ? 20 : 16; }
 
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<VEC>(), 1)
 // adds the slots k, k + W, ... and the W sums are added in warp order.  W is 8
 // where a group has few slots and 32 where it has many, which eight warps
 // would wait for one batch of loads after another (4,099 x 1,001 fp32, 148
-// slots: the whole backward 34.8 us with 8, 32.8 with 32).
+// slots: the whole backward 25.6 us with 8, 23.9 with 32).
 template <int W>
 __global__ void __launch_bounds__(32 * W) norm_reduce_kernel(const NormArgs a, float* dw, float* db) {
   __shared__ float sm[2][W][32];

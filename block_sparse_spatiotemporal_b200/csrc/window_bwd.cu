@@ -16,7 +16,8 @@
 // Warp 0 takes the CTA's next item from a counter, decodes it once and
 // publishes it in a ring (every warp decoding its own, items dealt out in
 // turn: 1,311 against 1,161 us at 12 heads, 16,384 tokens in frames of 1,024,
-// window 3 + 1), and loads the tiles by TMA.
+// window 3 + 1, one call at a time behind a flush of L2), and loads the tiles
+// by TMA.
 // Per step two warps issue S = X0 Y0^T and dP = X1 Y1^T (X stationary: K, V
 // or Q, dO; Y moving) into one of NB TMEM buffers, eight warps (two per TMEM
 // lane quarter, half the columns each) turn them into P and dS and write both
