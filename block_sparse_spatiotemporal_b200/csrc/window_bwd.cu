@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tbase = ctl->tmem_base;
   // The query-stationary kernel needs nothing of the key-stationary one in
   // front of it and starts on the SMs that one leaves (2 x 14 heads over 2,
-  // 1,531 tokens: 82 -> 64 us; 12 heads, 16,384 tokens: 1,160 -> 1,130 us);
+  // 1,531 tokens: 80 -> 63 us; 12 heads, 16,384 tokens: 1,157 -> 1,140 us, one
+  // call at a time behind a flush of L2);
   // what prep wrote is complete then, since every block of that one has waited
   // for it, and is read past L1.  It ends after that one, so that whatever
   // follows in the stream does too.
